@@ -341,6 +341,137 @@ qmm_status qmm_moe_routed(const qmm_weights* gate, const qmm_weights* up, const 
                           int64_t t, int64_t topk, uint16_t* out, void* ws, size_t ws_bytes,
                           void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Rows grouped by expert.  A prefill window's mixture-of-experts layer is
+ * qmm_route_rows, qmm_permute, qmm_grouped_swiglu, qmm_grouped_gemm,
+ * qmm_unpermute: the (token, slot) pairs are sorted by expert, every expert's
+ * rows lie together, and each expert's packed weights are decoded once for
+ * all of its rows ("Mark-Experimental-V3-8B", section "Mixture-of-Experts
+ * (MoE)").  For a decode step qmm_moe_routed is the faster call.
+ * ------------------------------------------------------------------------- */
+
+/* qmm_route with the inverse of its permutation: a stable counting sort of
+ * the t*topk pairs by expert.
+ *   topk_ids        device, [t][topk] int32; -1 is a pair without an expert
+ *                   (a padded token); any other id outside [0, num_experts)
+ *                   is left out too and records QMM_ERR_DEVICE_FAULT
+ *   expert_offsets  device, [num_experts+1] int32: the rows of expert e are
+ *                   offsets[e] .. offsets[e+1]-1
+ *   pair_perm       device, [t*topk] int32: the pair p = token*topk+slot of
+ *                   each row, p increasing within an expert; entries from
+ *                   offsets[num_experts] on are left as they were
+ *   pair_row        device, [t][topk] int32: the row of each pair, -1 for
+ *                   pairs without one
+ * Limits: num_experts <= 1024, t*topk < 2^30.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, NOT_SM100, CUDA. */
+qmm_status qmm_route_rows(const int32_t* topk_ids, int64_t t, int64_t topk, int64_t num_experts,
+                          int32_t* expert_offsets, int32_t* pair_perm, int32_t* pair_row, void* stream);
+
+/* The token rows in expert order: xs[pair_row[t][s]] = x[t].
+ *   x         device, [t][d] fp16 (any 2-byte values: they are copied)
+ *   pair_row  device, [t][topk] int32 from qmm_route_rows; rows outside
+ *             [0, t*topk) are skipped
+ *   xs        device, [t*topk][d] fp16; rows no pair has are left as they
+ *             were.  Must not overlap x.
+ * Limits: d % 8 == 0.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, NOT_SM100, CUDA. */
+qmm_status qmm_permute(const uint16_t* x, const int32_t* pair_row, int64_t t, int64_t topk, int64_t d, uint16_t* xs,
+                       void* stream);
+
+/* The gradient of qmm_permute: dx[t] = fp16(sum_s dxs[pair_row[t][s]]), the
+ * slots added in fp32 in slot order (0 for a token without rows).
+ *   dxs  device, [t*topk][d] fp16;  dx device, [t][d] fp16, written completely
+ * Limits and errors: as qmm_permute. */
+qmm_status qmm_permute_backward(const uint16_t* dxs, const int32_t* pair_row, int64_t t, int64_t topk, int64_t d,
+                                uint16_t* dx, void* stream);
+
+/* The rows back in token order, weighted and added: out[t] = fp16(sum_s
+ * topk_weights[t][s] * ys[pair_row[t][s]]), in fp32 in slot order; pairs
+ * without a row add nothing (0 for a token without rows).
+ *   ys            device, [t*topk][d] fp16
+ *   topk_weights  device, [t][topk] fp32, or NULL for weights of 1
+ *   out           device, [t][d] fp16, written completely
+ * Limits and errors: as qmm_permute. */
+qmm_status qmm_unpermute(const uint16_t* ys, const int32_t* pair_row, const float* topk_weights, int64_t t,
+                         int64_t topk, int64_t d, uint16_t* out, void* stream);
+
+/* The gradients of qmm_unpermute: for every pair p = (t, s) with row r,
+ * dys[r] = fp16(topk_weights[p] * dout[t]) and dweights[p] = sum_j ys[r][j]
+ * dout[t][j] in fp32 (the same bits every call); dweights[p] = 0 for pairs
+ * without a row, and rows of dys no pair has are left as they were.
+ *   dout          device, [t][d] fp16
+ *   ys            device, [t*topk][d] fp16, qmm_unpermute's input
+ *   topk_weights  device, [t][topk] fp32, or NULL for weights of 1
+ *   dys           device, [t*topk][d] fp16; must not overlap dout or ys
+ *   dweights      device, [t][topk] fp32, written completely
+ * Limits and errors: as qmm_permute. */
+qmm_status qmm_unpermute_backward(const uint16_t* dout, const uint16_t* ys, const int32_t* pair_row,
+                                  const float* topk_weights, int64_t t, int64_t topk, int64_t d, uint16_t* dys,
+                                  float* dweights, void* stream);
+
+/* The experts' products over sorted rows: ys[r] = W_e xs[r] for
+ * expert_offsets[e] <= r < expert_offsets[e+1], the weights decoded and the
+ * sum taken as in qmm_gemm.  Rows from expert_offsets[num_experts] on are
+ * neither read nor written.
+ *   experts         a stack of num_experts matrices, any format
+ *   xs              device, [rows][k] fp16
+ *   expert_offsets  device, [num_experts+1] int32, nondecreasing within
+ *                   0..rows (others are clamped and record
+ *                   QMM_ERR_DEVICE_FAULT)
+ *   ys              device, [rows][n] fp16
+ * Limits: num_experts <= 256.
+ * Errors: as qmm_grouped_gemv, except QMM_ERR_WORKSPACE. */
+qmm_status qmm_grouped_gemm(const qmm_weights* experts, const uint16_t* xs, const int32_t* expert_offsets,
+                            int64_t rows, uint16_t* ys, void* stream);
+
+/* Gate and up in one pass over the sorted rows: h[r] = fp16(SiLU(W_gate,e
+ * xs[r]) * (W_up,e xs[r])), SiLU(z) = z / (1 + e^-z), both sums and the
+ * product in fp32 (the h of qmm_moe_routed).
+ *   gate, up  stacks of num_experts matrices [n][k] (same format, n, k, E)
+ *   h         device, [rows][n] fp16
+ * Otherwise as qmm_grouped_gemm. */
+qmm_status qmm_grouped_swiglu(const qmm_weights* gate, const qmm_weights* up, const uint16_t* xs,
+                              const int32_t* expert_offsets, int64_t rows, uint16_t* h, void* stream);
+
+/* A pool of low-rank adapters of equal shape beside one projection ("1bit.gg
+ * zyphra": the graph form base + B*(A*x)).  Adapter l is A_l [rank][k] and
+ * B_l [n][rank]; with `ranks` it uses the first ranks[l] rows of A_l and
+ * columns of B_l (the others are never used, whatever they hold). */
+typedef struct {
+  int64_t num_adapters;  /* <= 1024 */
+  int64_t n;             /* output columns of the projection */
+  int64_t k;             /* input columns: k % 8 == 0 */
+  int64_t rank;          /* rank of the stacks: <= 256, a multiple of 8 */
+  const void* a;         /* device: fp16 [rank][k], a_stride bytes between adapters */
+  const void* b;         /* device: fp16 [n][rank], b_stride bytes between adapters */
+  const float* scales;   /* device: [num_adapters] fp32 (alpha / rank) */
+  const int32_t* ranks;  /* device: [num_adapters] int32 in 0..rank, or NULL */
+  int64_t a_stride;      /* multiples of 16, at least one adapter */
+  int64_t b_stride;
+} qmm_adapters;
+
+/* The adapters of many requests at once, beside a shared projection: for
+ * every row i with adapter a = adapter_ids[i],
+ *   y[i] = fp16(base[i] + scales[a] * B_a (A_a x[i])),
+ * both sums in fp32, one rounding; y[i] = base[i] for rows without an
+ * adapter.  base is the projection's output (qmm_gemv, qmm_gemm); y may be
+ * the same buffer.
+ *   x            device, [m][k] fp16
+ *   adapter_ids  device, [m] int32 in any order; -1 is a row without an
+ *                adapter, and so is any other id outside [0, num_adapters),
+ *                which records QMM_ERR_DEVICE_FAULT (as does a rank outside
+ *                0..rank, which is clamped)
+ *   base, y      device, [m][n] fp16: the same buffer or not overlapping
+ *   ws           device workspace of ws_bytes (qmm_lora_workspace_bytes);
+ *                two calls that may overlap on the GPU need one each
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, NOT_SM100, CUDA,
+ * WORKSPACE. */
+qmm_status qmm_lora(const qmm_adapters* adapters, const uint16_t* x, const int32_t* adapter_ids, int64_t m,
+                    const uint16_t* base, uint16_t* y, void* ws, size_t ws_bytes, void* stream);
+
+/* Device workspace bytes of qmm_lora for m rows (0 for sizes it refuses). */
+size_t qmm_lora_workspace_bytes(const qmm_adapters* adapters, int64_t m);
+
 enum { QMM_OP_DEQUANT = 0, QMM_OP_GEMV = 1, QMM_OP_GEMM = 2, QMM_OP_ROUTE = 3, QMM_OP_GROUPED = 4,
        QMM_OP_MOE = 5 };
 

@@ -5,6 +5,8 @@
 //
 // Step 1 (route): a stable counting sort of the t*topk (token, slot) pairs by
 // expert id -- offsets[E+1] and a pair permutation -- in one CTA.
+// (A null permutation: the rows are already sorted, pair = position, and the
+// offsets are the caller's, so they are clamped into the P rows there are.)
 // Step 2 (grouped GEMV): one warp per (expert, 16-row tile); the warp decodes
 // its weight tile once per k16 step into MMA fragments and multiplies it with
 // up to 32 gathered activation rows (4 MMA n-tiles) routed to that expert, so
@@ -12,6 +14,7 @@
 // y[token][slot][:] of each pair.
 #pragma once
 #include "k_gemv.cuh"
+#include "k_rows.cuh"
 #include "qmm_dev.cuh"
 
 namespace qmm {
@@ -79,12 +82,22 @@ __global__ void __launch_bounds__(kRouteThreads, 1)
 }
 
 // One warp per (expert, 16-row tile).  x rows: x[token] (x_per_pair == 0,
-// [t][k]) or x[pair] (x_per_pair == 1, [t*topk][k]).
-template <int FMT>
+// [t][k]) or x[pair] (x_per_pair == 1, [t*topk][k]).  SWI: the tile of two
+// stacks (gate: data, up: data2) and y = fp16(SiLU(gate) * up), SiLU(z) =
+// z / (1 + e^-z) in fp32.
+struct GroupedUp {  // SWI: the up stack
+  const uint8_t* data;
+  int64_t dstride;
+  const uint8_t* scales;
+  int64_t sstride;
+  float g;
+};
+template <int FMT, bool SWI = false>
 __global__ void __launch_bounds__(128) grouped_gemv_kernel(
     const uint8_t* __restrict__ data, int64_t dstride, const uint8_t* __restrict__ scales, int64_t sstride,
     float g, const uint16_t* __restrict__ x, int x_per_pair, int topk, const int32_t* __restrict__ offsets,
-    const int32_t* __restrict__ perm, uint16_t* __restrict__ y, int64_t n, int64_t k, int E) {
+    const int32_t* __restrict__ perm, int P, uint16_t* __restrict__ y, int64_t n, int64_t k, int E,
+    const GroupedUp up) {
   __shared__ uint32_t kvh[16];
   if (threadIdx.x < 16) kvh[threadIdx.x] = __half_as_ushort(__int2half_rn(c_iq4nl_kv[threadIdx.x]));
   __syncthreads();
@@ -93,11 +106,15 @@ __global__ void __launch_bounds__(128) grouped_gemv_kernel(
   const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int64_t e = item / tiles, tile = item % tiles;
   if (e >= E) return;
-  const int start = offsets[e];
-  const int cnt = offsets[e + 1] - start;
+  int start = 0, cnt = 0;
+  if (perm) {
+    start = offsets[e];
+    cnt = offsets[e + 1] - start;
+  } else {
+    cnt = group_range(offsets, (int)e, P, start);
+  }
   if (cnt <= 0) return;
-  const uint8_t* de = data + e * dstride;
-  const uint8_t* se = scales ? scales + e * sstride : nullptr;
+  constexpr int kMats = SWI ? 2 : 1;
   const int64_t r0 = tile * 16 + grp, r1 = r0 + 8;
   const float gs = (FMT == 3) ? g : 1.0f;
   for (int tok0 = 0; tok0 < cnt; tok0 += 32) {
@@ -109,21 +126,30 @@ __global__ void __launch_bounds__(128) grouped_gemv_kernel(
       const int slot = grp + 8 * j;
       xr[j] = nullptr;
       if (slot < ng) {
-        const int pair = perm[start + tok0 + slot];
+        const int pair = perm ? perm[start + tok0 + slot] : start + tok0 + slot;
         xr[j] = x + (int64_t)(x_per_pair ? pair : pair / topk) * k;
       }
     }
-    float acc[4][4];
+    float acc[kMats][4][4];
 #pragma unroll
-    for (int j = 0; j < 4; j++)
+    for (int q = 0; q < kMats; q++)
 #pragma unroll
-      for (int c = 0; c < 4; c++) acc[j][c] = 0.f;
+      for (int j = 0; j < 4; j++)
+#pragma unroll
+        for (int c = 0; c < 4; c++) acc[q][j][c] = 0.f;
     for (int64_t k0 = 0; k0 < k; k0 += 16) {
       const int64_t ka = k0 + 2 * tig, kb = ka + 8;
-      const uint32_t a0 = generic_pair<FMT>(de, se, r0, n, k, ka, kvh);
-      const uint32_t a1 = generic_pair<FMT>(de, se, r1, n, k, ka, kvh);
-      const uint32_t a2 = generic_pair<FMT>(de, se, r0, n, k, kb, kvh);
-      const uint32_t a3 = generic_pair<FMT>(de, se, r1, n, k, kb, kvh);
+      uint32_t a[kMats][4];
+#pragma unroll
+      for (int q = 0; q < kMats; q++) {
+        const uint8_t* de = q ? up.data + e * up.dstride : data + e * dstride;
+        const uint8_t* se = q ? (up.scales ? up.scales + e * up.sstride : nullptr)
+                              : (scales ? scales + e * sstride : nullptr);
+        a[q][0] = generic_pair<FMT>(de, se, r0, n, k, ka, kvh);
+        a[q][1] = generic_pair<FMT>(de, se, r1, n, k, ka, kvh);
+        a[q][2] = generic_pair<FMT>(de, se, r0, n, k, kb, kvh);
+        a[q][3] = generic_pair<FMT>(de, se, r1, n, k, kb, kvh);
+      }
 #pragma unroll
       for (int j = 0; j < 4; j++) {
         if (8 * j < ng) {
@@ -132,22 +158,26 @@ __global__ void __launch_bounds__(128) grouped_gemv_kernel(
             b0 = *reinterpret_cast<const uint32_t*>(xr[j] + ka);
             b1 = *reinterpret_cast<const uint32_t*>(xr[j] + kb);
           }
-          mma_16816(acc[j], a0, a1, a2, a3, b0, b1);
+#pragma unroll
+          for (int q = 0; q < kMats; q++) mma_16816(acc[q][j], a[q][0], a[q][1], a[q][2], a[q][3], b0, b1);
         }
       }
     }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      const int s0 = 8 * j + 2 * tig, s1 = s0 + 1;
-      if (s0 < ng) {
-        const int64_t pr = perm[start + tok0 + s0];
-        if (r0 < n) y[pr * n + r0] = f32_to_f16_bits(acc[j][0] * gs);
-        if (r1 < n) y[pr * n + r1] = f32_to_f16_bits(acc[j][2] * gs);
-      }
-      if (s1 < ng) {
-        const int64_t pr = perm[start + tok0 + s1];
-        if (r0 < n) y[pr * n + r0] = f32_to_f16_bits(acc[j][1] * gs);
-        if (r1 < n) y[pr * n + r1] = f32_to_f16_bits(acc[j][3] * gs);
+#pragma unroll
+      for (int h = 0; h < 2; h++) {  // token slots 8j + 2tig + h; values c = h (row r0), h + 2 (row r1)
+        const int slot = 8 * j + 2 * tig + h;
+        if (slot >= ng) continue;
+        float v0 = acc[0][j][h] * gs, v1 = acc[0][j][h + 2] * gs;
+        if (SWI) {
+          const float gu = (FMT == 3) ? up.g : 1.0f;
+          v0 = v0 / (1.0f + expf(-v0)) * (acc[kMats - 1][j][h] * gu);
+          v1 = v1 / (1.0f + expf(-v1)) * (acc[kMats - 1][j][h + 2] * gu);
+        }
+        const int64_t pr = perm ? perm[start + tok0 + slot] : start + tok0 + slot;
+        if (r0 < n) y[pr * n + r0] = f32_to_f16_bits(v0);
+        if (r1 < n) y[pr * n + r1] = f32_to_f16_bits(v1);
       }
     }
   }

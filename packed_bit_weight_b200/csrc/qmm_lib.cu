@@ -22,6 +22,7 @@
 #include "k_gemm.cuh"
 #include "k_grouped.cuh"
 #include "k_iq4t.cuh"
+#include "k_lora.cuh"
 #include "k_quant.cuh"
 #include "k_moe.cuh"
 
@@ -699,17 +700,29 @@ static qmm_status launch_iq4_stream(const qmm_weights* w, const uint16_t* x, int
   return launch_iq4_mode<IQ_OUT_F16>(w, nullptr, x, x_per_pair, topk, offsets, perm, m_plain, y, nullptr, st, di);
 }
 
+// P: the rows there are, when perm is null (rows already sorted).  up: the
+// second stack of the SwiGLU product.
 template <int FMT>
 static qmm_status launch_grouped(const qmm_weights* w, const uint16_t* x, int x_per_pair, int64_t topk,
-                                 const int32_t* offsets, const int32_t* perm, uint16_t* y, cudaStream_t st) {
+                                 const int32_t* offsets, const int32_t* perm, uint16_t* y, cudaStream_t st,
+                                 int64_t P = 0, const qmm_weights* up = nullptr) {
   const int64_t tiles = (w->n + 15) / 16;
   const int64_t items = tiles * w->num_experts;
   const int64_t blocks = (items + 3) / 4;
   if (blocks > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
-  grouped_gemv_kernel<FMT><<<(unsigned)blocks, 128, 0, st>>>(
+  GroupedUp u = {};
+  if (up) {
+    u.data = static_cast<const uint8_t*>(up->data);
+    u.dstride = up->expert_data_stride;
+    u.scales = static_cast<const uint8_t*>(up->scales);
+    u.sstride = up->expert_scale_stride;
+    u.g = up->global_scale;
+  }
+  auto kern = up ? grouped_gemv_kernel<FMT, true> : grouped_gemv_kernel<FMT, false>;
+  kern<<<(unsigned)blocks, 128, 0, st>>>(
       static_cast<const uint8_t*>(w->data), w->expert_data_stride, static_cast<const uint8_t*>(w->scales),
-      w->expert_scale_stride, w->global_scale, x, x_per_pair, (int)topk, offsets, perm, y, w->n, w->k,
-      (int)w->num_experts);
+      w->expert_scale_stride, w->global_scale, x, x_per_pair, (int)topk, offsets, perm, (int)P, y, w->n, w->k,
+      (int)w->num_experts, u);
   return launch_status();
 }
 
@@ -1282,6 +1295,283 @@ qmm_status qmm_moe_routed(const qmm_weights* gate, const qmm_weights* up, const 
                  (const float*)yg, topk_ids, (int)E, (int)t, (int)topk, (int)d, out) != cudaSuccess)
     return QMM_ERR_CUDA;
   set_variant("moe:route+gate_up_swiglu_iq4+down_scaled_iq4+combine");
+  return launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Rows grouped by expert
+// ---------------------------------------------------------------------------
+// CTAs of the sort's cluster: one up to 1,024 pairs, then as many as keep a
+// warp at two 32-pair steps, at most 8 (the portable cluster size).
+static int sort_ctas(int64_t P) {
+  int c = 1;
+  while (c < 8 && P > (int64_t)c * kRowsSortThreads * 2) c *= 2;
+  return c;
+}
+
+static qmm_status launch_route_rows(const int32_t* ids, int64_t P, int64_t E, int32_t* offsets, int32_t* perm,
+                                    int32_t* row_of, cudaStream_t st) {
+  const int smem = route_rows_smem((int)E);
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(route_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               route_rows_smem(kRowsMaxBins)) != cudaSuccess)
+    return QMM_ERR_CUDA;
+  const int cs = sort_ctas(P);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cs);
+  cfg.blockDim = dim3(kRowsSortThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, route_rows_kernel, ids, (int)P, (int)E, offsets, perm, row_of) != cudaSuccess)
+    return QMM_ERR_CUDA;
+  return launch_status();
+}
+
+qmm_status qmm_route_rows(const int32_t* topk_ids, int64_t t, int64_t topk, int64_t num_experts,
+                          int32_t* expert_offsets, int32_t* pair_perm, int32_t* pair_row, void* stream) {
+  if (t < 0 || topk < 0 || num_experts < 1) return QMM_ERR_INVALID_ARG;
+  if (num_experts > kRowsMaxBins || (topk > 0 && t > (INT32_MAX / 2) / topk)) return QMM_ERR_UNSUPPORTED_SHAPE;
+  const int64_t P = t * topk;
+  if (!expert_offsets || (P > 0 && (!topk_ids || !pair_perm || !pair_row))) return QMM_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)topk_ids, (const void*)expert_offsets, (const void*)pair_perm,
+                        (const void*)pair_row})
+    if (p && !aligned16(p)) return QMM_ERR_MISALIGNED;
+  DevInfo* di = nullptr;
+  qmm_status s = device_info(&di);
+  if (s != QMM_OK) return s;
+  s = launch_route_rows(topk_ids, P, num_experts, expert_offsets, pair_perm, pair_row,
+                        static_cast<cudaStream_t>(stream));
+  if (s == QMM_OK) set_variant("route_rows<cluster=%d>", sort_ctas(P));
+  return s;
+}
+
+// Sizes shared by the row movers; *P = t * topk.
+static qmm_status check_rows(int64_t t, int64_t topk, int64_t d, int64_t* P) {
+  if (t < 0 || topk < 0 || d < 0) return QMM_ERR_INVALID_ARG;
+  if (d % 8 || d > INT32_MAX / 2 || (topk > 0 && t > (INT32_MAX / 2) / topk) || t > INT32_MAX / 2)
+    return QMM_ERR_UNSUPPORTED_SHAPE;
+  *P = t * topk;
+  return QMM_OK;
+}
+
+// 16-byte chunks per lane: wide rows and many tokens take 4 (fewer warps, more
+// bytes in flight each), a few tokens 1 (more warps).
+static int row_unroll(int64_t t, int64_t d8, int sms) {
+  const int64_t warps1 = t * ((d8 + 31) / 32);
+  return warps1 >= (int64_t)sms * 64 ? 4 : warps1 >= (int64_t)sms * 16 ? 2 : 1;
+}
+
+static qmm_status row_grid(int64_t t, int64_t d8, int u, int* segs, unsigned* blocks) {
+  *segs = (int)((d8 + 32 * u - 1) / (32 * u));
+  const int64_t b = (t * *segs + 7) / 8;
+  if (b > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
+  *blocks = (unsigned)b;
+  return QMM_OK;
+}
+
+qmm_status qmm_permute(const uint16_t* x, const int32_t* pair_row, int64_t t, int64_t topk, int64_t d, uint16_t* xs,
+                       void* stream) {
+  int64_t P = 0;
+  qmm_status s = check_rows(t, topk, d, &P);
+  if (s != QMM_OK) return s;
+  if (P > 0 && d > 0 && (!x || !pair_row || !xs)) return QMM_ERR_INVALID_ARG;
+  if ((x && !aligned16(x)) || (pair_row && !aligned16(pair_row)) || (xs && !aligned16(xs))) return QMM_ERR_MISALIGNED;
+  DevInfo* di = nullptr;
+  if ((s = device_info(&di)) != QMM_OK) return s;
+  if (P == 0 || d == 0) return QMM_OK;
+  const int64_t d8 = d / 8;
+  const int u = row_unroll(t, d8, di->sms);
+  int segs = 0;
+  unsigned blocks = 0;
+  if ((s = row_grid(t, d8, u, &segs, &blocks)) != QMM_OK) return s;
+  auto kern = u == 4 ? permute_kernel<4> : u == 2 ? permute_kernel<2> : permute_kernel<1>;
+  if (launch_pdl(kern, dim3(blocks), dim3(256), 0, static_cast<cudaStream_t>(stream),
+                 reinterpret_cast<const uint4*>(x), pair_row, t, (int)topk, (int)d8, segs, (int)P,
+                 reinterpret_cast<uint4*>(xs)) != cudaSuccess)
+    return QMM_ERR_CUDA;
+  set_variant("permute<u=%d>", u);
+  return launch_status();
+}
+
+static qmm_status launch_unpermute(const uint16_t* ys, const int32_t* pair_row, const float* gw, int64_t t,
+                                   int64_t topk, int64_t d, uint16_t* out, void* stream, const char* name) {
+  int64_t P = 0;
+  qmm_status s = check_rows(t, topk, d, &P);
+  if (s != QMM_OK) return s;
+  if (t > 0 && d > 0 && (!out || (topk > 0 && (!ys || !pair_row)))) return QMM_ERR_INVALID_ARG;
+  if ((ys && !aligned16(ys)) || (pair_row && !aligned16(pair_row)) || (gw && !aligned16(gw)) ||
+      (out && !aligned16(out)))
+    return QMM_ERR_MISALIGNED;
+  DevInfo* di = nullptr;
+  if ((s = device_info(&di)) != QMM_OK) return s;
+  if (t == 0 || d == 0) return QMM_OK;
+  const int64_t d8 = d / 8;
+  const int u = row_unroll(t, d8, di->sms);
+  int segs = 0;
+  unsigned blocks = 0;
+  if ((s = row_grid(t, d8, u, &segs, &blocks)) != QMM_OK) return s;
+  auto kern = u == 4 ? unpermute_kernel<4> : u == 2 ? unpermute_kernel<2> : unpermute_kernel<1>;
+  if (launch_pdl(kern, dim3(blocks), dim3(256), 0, static_cast<cudaStream_t>(stream),
+                 reinterpret_cast<const uint4*>(ys), pair_row, gw, t, (int)topk, (int)d8, segs, (int)P,
+                 reinterpret_cast<uint4*>(out)) != cudaSuccess)
+    return QMM_ERR_CUDA;
+  set_variant("%s<u=%d>", name, u);
+  return launch_status();
+}
+
+qmm_status qmm_permute_backward(const uint16_t* dxs, const int32_t* pair_row, int64_t t, int64_t topk, int64_t d,
+                                uint16_t* dx, void* stream) {
+  return launch_unpermute(dxs, pair_row, nullptr, t, topk, d, dx, stream, "permute_backward");
+}
+
+qmm_status qmm_unpermute(const uint16_t* ys, const int32_t* pair_row, const float* topk_weights, int64_t t,
+                         int64_t topk, int64_t d, uint16_t* out, void* stream) {
+  return launch_unpermute(ys, pair_row, topk_weights, t, topk, d, out, stream, "unpermute");
+}
+
+qmm_status qmm_unpermute_backward(const uint16_t* dout, const uint16_t* ys, const int32_t* pair_row,
+                                  const float* topk_weights, int64_t t, int64_t topk, int64_t d, uint16_t* dys,
+                                  float* dweights, void* stream) {
+  int64_t P = 0;
+  qmm_status s = check_rows(t, topk, d, &P);
+  if (s != QMM_OK) return s;
+  if (P > 0 && (!pair_row || !dweights || (d > 0 && (!dout || !ys || !dys)))) return QMM_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)dout, (const void*)ys, (const void*)pair_row, (const void*)topk_weights,
+                        (const void*)dys, (const void*)dweights})
+    if (p && !aligned16(p)) return QMM_ERR_MISALIGNED;
+  DevInfo* di = nullptr;
+  if ((s = device_info(&di)) != QMM_OK) return s;
+  if (P == 0) return QMM_OK;
+  if (launch_pdl(unpermute_backward_kernel, dim3((unsigned)((P + 7) / 8)), dim3(256), 0,
+                 static_cast<cudaStream_t>(stream), reinterpret_cast<const uint4*>(dout),
+                 reinterpret_cast<const uint4*>(ys), pair_row, topk_weights, P, (int)topk, (int)(d / 8),
+                 reinterpret_cast<uint4*>(dys), dweights) != cudaSuccess)
+    return QMM_ERR_CUDA;
+  set_variant("unpermute_backward");
+  return launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Experts' products over sorted rows
+// ---------------------------------------------------------------------------
+static qmm_status check_grouped_rows(const qmm_weights* w, const uint16_t* xs, const int32_t* offsets, int64_t rows,
+                                     const uint16_t* ys) {
+  qmm_status s = check_weights(w, true);
+  if (s != QMM_OK) return s;
+  if ((s = check_expert_strides(w)) != QMM_OK) return s;
+  if (rows < 0) return QMM_ERR_INVALID_ARG;
+  if (w->num_experts > kRouteMaxExperts || rows > INT32_MAX / 2) return QMM_ERR_UNSUPPORTED_SHAPE;
+  if (rows > 0 && w->n > 0 && (!offsets || !ys || (w->k > 0 && !xs))) return QMM_ERR_INVALID_ARG;
+  if ((offsets && !aligned16(offsets)) || (ys && !aligned16(ys)) || (xs && !aligned16(xs))) return QMM_ERR_MISALIGNED;
+  return QMM_OK;
+}
+
+// up: the second stack of the SwiGLU product, or null.
+static qmm_status grouped_rows(const qmm_weights* w, const qmm_weights* up, const uint16_t* xs,
+                               const int32_t* offsets, int64_t rows, uint16_t* ys, cudaStream_t st,
+                               const DevInfo* di) {
+  qmm_status s;
+  switch (w->fmt) {
+    case QMM_FMT_IQ4_NL: s = launch_grouped<1>(w, xs, 1, 1, offsets, nullptr, ys, st, rows, up); break;
+    case QMM_FMT_FP4G16_F16: s = launch_grouped<2>(w, xs, 1, 1, offsets, nullptr, ys, st, rows, up); break;
+    case QMM_FMT_MXFP4: s = launch_grouped<4>(w, xs, 1, 1, offsets, nullptr, ys, st, rows, up); break;
+    default: s = launch_grouped<3>(w, xs, 1, 1, offsets, nullptr, ys, st, rows, up); break;
+  }
+  if (s == QMM_OK) set_variant("%s_generic<fmt=%d>", up ? "grouped_swiglu" : "grouped_gemm", w->fmt);
+  return s;
+}
+
+qmm_status qmm_grouped_gemm(const qmm_weights* experts, const uint16_t* xs, const int32_t* expert_offsets,
+                            int64_t rows, uint16_t* ys, void* stream) {
+  qmm_status s = check_grouped_rows(experts, xs, expert_offsets, rows, ys);
+  if (s != QMM_OK) return s;
+  DevInfo* di = nullptr;
+  if ((s = device_info(&di)) != QMM_OK) return s;
+  if (rows == 0 || experts->n == 0) return QMM_OK;
+  return grouped_rows(experts, nullptr, xs, expert_offsets, rows, ys, static_cast<cudaStream_t>(stream), di);
+}
+
+qmm_status qmm_grouped_swiglu(const qmm_weights* gate, const qmm_weights* up, const uint16_t* xs,
+                              const int32_t* expert_offsets, int64_t rows, uint16_t* h, void* stream) {
+  qmm_status s = check_grouped_rows(gate, xs, expert_offsets, rows, h);
+  if (s != QMM_OK) return s;
+  if ((s = check_grouped_rows(up, xs, expert_offsets, rows, h)) != QMM_OK) return s;
+  if (up->fmt != gate->fmt || up->n != gate->n || up->k != gate->k || up->num_experts != gate->num_experts)
+    return QMM_ERR_INVALID_ARG;
+  DevInfo* di = nullptr;
+  if ((s = device_info(&di)) != QMM_OK) return s;
+  if (rows == 0 || gate->n == 0) return QMM_OK;
+  return grouped_rows(gate, up, xs, expert_offsets, rows, h, static_cast<cudaStream_t>(stream), di);
+}
+
+// ---------------------------------------------------------------------------
+// Low-rank adapters
+// ---------------------------------------------------------------------------
+static qmm_status check_adapters(const qmm_adapters* ad) {
+  if (!ad || ad->num_adapters < 1 || ad->n < 0 || ad->k < 0 || ad->rank < 0) return QMM_ERR_INVALID_ARG;
+  if (ad->num_adapters > kRowsMaxBins || ad->n > INT32_MAX / 2 || ad->k > INT32_MAX / 2 || ad->rank > kLoraMaxRank ||
+      ad->k % 8 || ad->rank % 8)
+    return QMM_ERR_UNSUPPORTED_SHAPE;
+  if (!ad->scales) return QMM_ERR_INVALID_ARG;
+  if ((ad->rank > 0 && ad->k > 0 && !ad->a) || (ad->rank > 0 && ad->n > 0 && !ad->b)) return QMM_ERR_INVALID_ARG;
+  if (ad->num_adapters > 1 &&
+      (ad->a_stride < 2 * ad->rank * ad->k || ad->b_stride < 2 * ad->rank * ad->n))
+    return QMM_ERR_INVALID_ARG;
+  if ((ad->a_stride & 15) || (ad->b_stride & 15)) return QMM_ERR_MISALIGNED;
+  for (const void* p : {(const void*)ad->a, (const void*)ad->b, (const void*)ad->scales, (const void*)ad->ranks})
+    if (p && !aligned16(p)) return QMM_ERR_MISALIGNED;
+  return QMM_OK;
+}
+
+size_t qmm_lora_workspace_bytes(const qmm_adapters* ad, int64_t m) {
+  if (check_adapters(ad) != QMM_OK || m < 0 || m > INT32_MAX / 2) return 0;
+  return align256(4 * (size_t)m * (size_t)ad->rank);
+}
+
+qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* adapter_ids, int64_t m,
+                    const uint16_t* base, uint16_t* y, void* ws, size_t ws_bytes, void* stream) {
+  qmm_status s = check_adapters(ad);
+  if (s != QMM_OK) return s;
+  if (m < 0) return QMM_ERR_INVALID_ARG;
+  if (m > INT32_MAX / 2) return QMM_ERR_UNSUPPORTED_SHAPE;
+  DevInfo* di = nullptr;
+  if (m > 0 && ad->n > 0 && (!adapter_ids || !base || !y || (ad->k > 0 && !x))) return QMM_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)x, (const void*)adapter_ids, (const void*)base, (const void*)y, (const void*)ws})
+    if (p && !aligned16(p)) return QMM_ERR_MISALIGNED;
+  if ((s = device_info(&di)) != QMM_OK) return s;
+  if (m == 0 || ad->n == 0) return QMM_OK;
+  if (ws_bytes < qmm_lora_workspace_bytes(ad, m) || (!ws && ws_bytes)) return QMM_ERR_WORKSPACE;
+  LoraArgs a;
+  a.a = static_cast<const uint16_t*>(ad->a);
+  a.b = static_cast<const uint16_t*>(ad->b);
+  a.scales = ad->scales;
+  a.ranks = ad->ranks;
+  a.a_stride = ad->a_stride;
+  a.b_stride = ad->b_stride;
+  a.L = (int)ad->num_adapters;
+  a.R = (int)ad->rank;
+  a.n = (int)ad->n;
+  a.k = (int)ad->k;
+  a.m = (int)m;
+  a.ids = adapter_ids;
+  a.x = x;
+  a.base = base;
+  a.y = y;
+  a.h = static_cast<float*>(ws);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t b1 = (m * ad->rank + 7) / 8, b2 = (m * ad->n + 255) / 256;
+  if (b1 > INT32_MAX || b2 > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
+  if (b1 && launch_pdl(lora_shrink_simple_kernel, dim3((unsigned)b1), dim3(256), 0, st, a) != cudaSuccess)
+    return QMM_ERR_CUDA;
+  if (launch_pdl(lora_expand_simple_kernel, dim3((unsigned)b2), dim3(256), 0, st, a) != cudaSuccess)
+    return QMM_ERR_CUDA;
+  set_variant("lora_simple");
   return launch_status();
 }
 

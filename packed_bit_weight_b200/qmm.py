@@ -43,6 +43,13 @@ class qmm_weights(ctypes.Structure):
                 ("expert_data_stride", ctypes.c_int64), ("expert_scale_stride", ctypes.c_int64)]
 
 
+class qmm_adapters(ctypes.Structure):
+    _fields_ = [("num_adapters", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("rank", ctypes.c_int64), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("ranks", ctypes.c_void_p), ("a_stride", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64)]
+
+
 _L = None
 LIB_PATH = _build.LIB
 
@@ -55,6 +62,7 @@ def _lib():
         L = ctypes.CDLL(LIB_PATH)
         vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
         W = ctypes.POINTER(qmm_weights)
+        A = ctypes.POINTER(qmm_adapters)
         sigs = {
             "qmm_data_bytes": (sz, [i32, i64, i64]),
             "qmm_scale_bytes": (sz, [i32, i64, i64]),
@@ -69,6 +77,15 @@ def _lib():
             "qmm_grouped_gemv_noalloc": (i32, [W, vp, i32, vp, i64, i64, vp, vp]),
             "qmm_router_topk": (i32, [vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp]),
             "qmm_moe_routed": (i32, [W, W, W, vp, vp, vp, i64, i64, vp, vp, sz, vp]),
+            "qmm_route_rows": (i32, [vp, i64, i64, i64, vp, vp, vp, vp]),
+            "qmm_permute": (i32, [vp, vp, i64, i64, i64, vp, vp]),
+            "qmm_permute_backward": (i32, [vp, vp, i64, i64, i64, vp, vp]),
+            "qmm_unpermute": (i32, [vp, vp, vp, i64, i64, i64, vp, vp]),
+            "qmm_unpermute_backward": (i32, [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp]),
+            "qmm_grouped_gemm": (i32, [W, vp, vp, i64, vp, vp]),
+            "qmm_grouped_swiglu": (i32, [W, W, vp, vp, i64, vp, vp]),
+            "qmm_lora": (i32, [A, vp, vp, i64, vp, vp, vp, sz, vp]),
+            "qmm_lora_workspace_bytes": (sz, [A, i64]),
             "qmm_workspace_bytes": (sz, [i32, W, i64, i64, i64]),
             "qmm_sync_check": (i32, [vp]),
             "qmm_debug_set": (i32, [i32, i64]),
@@ -366,6 +383,178 @@ def qmm_moe_routed(gate: PackedWeights, up: PackedWeights, down: PackedWeights, 
                                  _ptr(topk_ids, 4, "topk_ids"), _ptr(topk_weights, 4, "topk_weights"), t, topk,
                                  _ptr(out, 2, "out"), wp, wb, _stream(stream)), "qmm_moe_routed")
     return out
+
+
+# -- rows grouped by expert ------------------------------------------------------
+def _here(t: torch.Tensor | None, esize: int | None, name: str):
+    """_ptr for a tensor that must be on the current device (the C ABI
+    launches there, whatever device the pointer is of)."""
+    p = _ptr(t, esize, name)
+    if t is not None and t.device.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
+    return p
+
+
+def qmm_route_rows(topk_ids: torch.Tensor, num_experts: int, offsets: torch.Tensor, perm: torch.Tensor,
+                   rows: torch.Tensor, stream=None):
+    """qmm_route with the row of every pair (the inverse of perm): topk_ids
+    [t][topk] -> offsets [num_experts+1], perm [t*topk], rows [t][topk]."""
+    t, topk = topk_ids.shape
+    _need(offsets, 4 * (num_experts + 1), "offsets")
+    _need(perm, 4 * t * topk, "perm")
+    _need(rows, 4 * t * topk, "rows")
+    _check(_lib().qmm_route_rows(_here(topk_ids, 4, "topk_ids"), t, topk, num_experts, _here(offsets, 4, "offsets"),
+                                 _here(perm, 4, "perm"), _here(rows, 4, "rows"), _stream(stream)), "qmm_route_rows")
+    return offsets, perm, rows
+
+
+def _need_rows(rows: torch.Tensor, tok: torch.Tensor, tok_name: str, sorted_rows, weights=None):
+    """(t, topk, d) of a row mover: tok is [t][d], every tensor of
+    sorted_rows holds t*topk rows of d."""
+    t, topk = rows.shape
+    if tok.dim() != 2 or tok.shape[0] != t:
+        raise ValueError("%s must be [t][d] for rows of %d tokens" % (tok_name, t))
+    d = tok.shape[1]
+    for s, name in sorted_rows:
+        _need(s, 2 * t * topk * d, name)
+    for w, name in weights or ():
+        _need(w, 4 * t * topk, name)
+    return t, topk, d
+
+
+def qmm_permute(x: torch.Tensor, rows: torch.Tensor, xs: torch.Tensor, stream=None) -> torch.Tensor:
+    """xs[rows[t][s]] = x[t]: x [t][d] -> xs [t*topk][d]."""
+    t, topk, d = _need_rows(rows, x, "x", ((xs, "xs"),))
+    _check(_lib().qmm_permute(_here(x, 2, "x"), _here(rows, 4, "rows"), t, topk, d, _here(xs, 2, "xs"),
+                              _stream(stream)), "qmm_permute")
+    return xs
+
+
+def qmm_permute_backward(dxs: torch.Tensor, rows: torch.Tensor, dx: torch.Tensor, stream=None) -> torch.Tensor:
+    """dx[t] = sum_s dxs[rows[t][s]]: the gradient of qmm_permute."""
+    t, topk, d = _need_rows(rows, dx, "dx", ((dxs, "dxs"),))
+    _check(_lib().qmm_permute_backward(_here(dxs, 2, "dxs"), _here(rows, 4, "rows"), t, topk, d, _here(dx, 2, "dx"),
+                                       _stream(stream)), "qmm_permute_backward")
+    return dx
+
+
+def qmm_unpermute(ys: torch.Tensor, rows: torch.Tensor, topk_weights: torch.Tensor | None, out: torch.Tensor,
+                  stream=None) -> torch.Tensor:
+    """out[t] = sum_s topk_weights[t][s] * ys[rows[t][s]] (weights of 1 when
+    None): ys [t*topk][d] -> out [t][d]."""
+    t, topk, d = _need_rows(rows, out, "out", ((ys, "ys"),), ((topk_weights, "topk_weights"),))
+    _check(_lib().qmm_unpermute(_here(ys, 2, "ys"), _here(rows, 4, "rows"), _here(topk_weights, 4, "topk_weights"),
+                                t, topk, d, _here(out, 2, "out"), _stream(stream)), "qmm_unpermute")
+    return out
+
+
+def qmm_unpermute_backward(dout: torch.Tensor, ys: torch.Tensor, rows: torch.Tensor,
+                           topk_weights: torch.Tensor | None, dys: torch.Tensor, dweights: torch.Tensor,
+                           stream=None):
+    """The gradients of qmm_unpermute: dys [t*topk][d] and dweights [t][topk]."""
+    t, topk, d = _need_rows(rows, dout, "dout", ((ys, "ys"), (dys, "dys")),
+                            ((topk_weights, "topk_weights"), (dweights, "dweights")))
+    _check(_lib().qmm_unpermute_backward(_here(dout, 2, "dout"), _here(ys, 2, "ys"), _here(rows, 4, "rows"),
+                                         _here(topk_weights, 4, "topk_weights"), t, topk, d, _here(dys, 2, "dys"),
+                                         _here(dweights, 4, "dweights"), _stream(stream)), "qmm_unpermute_backward")
+    return dys, dweights
+
+
+def qmm_grouped_gemm(w: PackedWeights, xs: torch.Tensor, offsets: torch.Tensor, ys: torch.Tensor,
+                     stream=None) -> torch.Tensor:
+    """ys[r] = W_e xs[r] for the rows offsets[e] <= r < offsets[e+1]."""
+    d = w.desc()
+    _need(xs, 2 * xs.shape[0] * w.k, "xs")
+    _need(ys, 2 * xs.shape[0] * w.n, "ys")
+    _need(offsets, 4 * (w.experts + 1), "offsets")
+    _check(_lib().qmm_grouped_gemm(ctypes.byref(d), _here(xs, 2, "xs"), _here(offsets, 4, "offsets"), xs.shape[0],
+                                   _here(ys, 2, "ys"), _stream(stream)), "qmm_grouped_gemm")
+    return ys
+
+
+def qmm_grouped_swiglu(gate: PackedWeights, up: PackedWeights, xs: torch.Tensor, offsets: torch.Tensor,
+                       h: torch.Tensor, stream=None) -> torch.Tensor:
+    """h[r] = SiLU(W_gate,e xs[r]) * (W_up,e xs[r]) over the sorted rows."""
+    dg, du = gate.desc(), up.desc()
+    _need(xs, 2 * xs.shape[0] * gate.k, "xs")
+    _need(h, 2 * xs.shape[0] * gate.n, "h")
+    _need(offsets, 4 * (gate.experts + 1), "offsets")
+    _check(_lib().qmm_grouped_swiglu(ctypes.byref(dg), ctypes.byref(du), _here(xs, 2, "xs"),
+                                     _here(offsets, 4, "offsets"), xs.shape[0], _here(h, 2, "h"),
+                                     _stream(stream)), "qmm_grouped_swiglu")
+    return h
+
+
+# -- low-rank adapters -------------------------------------------------------------
+@dataclass
+class Adapters:
+    """Device tensors of a pool of low-rank adapters plus its C descriptor:
+    a [L][rank][k] and b [L][n][rank] (fp16; adapters may be further apart
+    than their size), scales [L] fp32, ranks [L] int32 or None."""
+    a: torch.Tensor
+    b: torch.Tensor
+    scales: torch.Tensor
+    ranks: torch.Tensor | None = None
+
+    def desc(self) -> qmm_adapters:
+        """The C descriptor, rebuilt only when a tensor was replaced or moved."""
+        key = tuple(None if t is None else (t.data_ptr(), t.shape, t.stride(), t.device)
+                    for t in (self.a, self.b, self.scales, self.ranks)) + (torch.cuda.current_device()
+                                                                           if self.a.is_cuda else None,)
+        cached = self.__dict__.get("_desc")
+        if cached is not None and cached[0] == key:
+            return cached[1]
+        d = self._build_desc()
+        self.__dict__["_desc"] = (key, d)
+        return d
+
+    def _build_desc(self) -> qmm_adapters:
+        a, b = self.a, self.b
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise ValueError("a must be [L][rank][k] and b [L][n][rank]")
+        L, R, k = a.shape
+        n = b.shape[1]
+        for t, name in ((a, "a"), (b, "b")):
+            if t.numel() and not t[0].is_contiguous():
+                raise ValueError("%s must have contiguous adapters" % name)
+        _need(self.scales, 4 * L, "scales")
+        _need(self.ranks, 4 * L, "ranks")
+        d = qmm_adapters()
+        d.num_adapters, d.n, d.k, d.rank = L, n, k, R
+        for t, name in ((a, "a"), (b, "b")):
+            if not t.is_cuda:
+                raise ValueError("%s must be a CUDA tensor" % name)
+            if t.element_size() != 2:
+                raise ValueError("%s must have 2-byte elements" % name)
+            if t.device.index != torch.cuda.current_device():
+                raise ValueError("%s is on %s, the current device is cuda:%d" %
+                                 (name, t.device, torch.cuda.current_device()))
+        d.a, d.b = ctypes.c_void_p(a.data_ptr()), ctypes.c_void_p(b.data_ptr())
+        d.a_stride = 2 * (a.stride(0) if L > 1 else R * k)
+        d.b_stride = 2 * (b.stride(0) if L > 1 else n * R)
+        d.scales, d.ranks = _here(self.scales, 4, "scales"), _here(self.ranks, 4, "ranks")
+        return d
+
+
+def qmm_lora_workspace_bytes(adapters: Adapters, m: int) -> int:
+    return _lib().qmm_lora_workspace_bytes(ctypes.byref(adapters.desc()), m)
+
+
+def qmm_lora(adapters: Adapters, x: torch.Tensor, adapter_ids: torch.Tensor, base: torch.Tensor, y: torch.Tensor,
+             ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[i] = base[i] + scale_a B_a (A_a x[i]) with a = adapter_ids[i]
+    (y[i] = base[i] for -1); y may be base."""
+    m, n, k = adapter_ids.numel(), adapters.b.shape[1], adapters.a.shape[2]
+    _need(x, 2 * m * k, "x")
+    _need(base, 2 * m * n, "base")
+    _need(y, 2 * m * n, "y")
+    d = adapters.desc()
+    wp, wb = _ws(ws)
+    if ws is not None:
+        _here(ws, None, "ws")
+    _check(_lib().qmm_lora(ctypes.byref(d), _here(x, 2, "x"), _here(adapter_ids, 4, "adapter_ids"), m,
+                           _here(base, 2, "base"), _here(y, 2, "y"), wp, wb, _stream(stream)), "qmm_lora")
+    return y
 
 
 DEBUG_WAIT_LIMIT_NS = 1
