@@ -22,6 +22,7 @@
 #include "k_gemm.cuh"
 #include "k_grouped.cuh"
 #include "k_iq4t.cuh"
+#include "k_ggemm.cuh"
 #include "k_lora.cuh"
 #include "k_quant.cuh"
 #include "k_moe.cuh"
@@ -724,6 +725,53 @@ static qmm_status launch_grouped(const qmm_weights* w, const uint16_t* x, int x_
       w->expert_scale_stride, w->global_scale, x, x_per_pair, (int)topk, offsets, perm, (int)P, y, w->n, w->k,
       (int)w->num_experts, u);
   return launch_status();
+}
+
+// Experts' products over sorted rows on tensor cores (k_ggemm.cuh; k % 128 == 0).
+template <int FMT, bool SWI>
+static qmm_status launch_grouped_gemm(const qmm_weights* w, const qmm_weights* up, const uint16_t* xs,
+                                      const int32_t* offsets, int64_t rows, uint16_t* ys, cudaStream_t st,
+                                      const DevInfo* di) {
+  CUtensorMap tx;
+  if (!make_map_2d(&tx, xs, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, (uint64_t)w->k, (uint64_t)rows, kGemmBK, 64,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+    return QMM_ERR_CUDA;
+  const size_t smem = GgSmem<FMT>::total();
+  if (smem > di->smem_optin) return QMM_ERR_CUDA;
+  auto kern = grouped_gemm_kernel<FMT, SWI>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return QMM_ERR_CUDA;
+  // at most this many row tiles (experts with rows plus whole tiles)
+  const int64_t row_tiles = rows / kGgTok + std::min(rows, w->num_experts);
+  const int64_t tiles = row_tiles * ((w->n + (SWI ? 63 : 127)) / (SWI ? 64 : 128));
+  if (tiles > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
+  const int grid = tiles < di->sms ? (int)tiles : di->sms;
+  GgArgs a = {};
+  const qmm_weights* ws[2] = {w, up ? up : w};
+  for (int i = 0; i < 2; i++) {
+    a.data[i] = static_cast<const uint8_t*>(ws[i]->data);
+    a.scales[i] = static_cast<const uint8_t*>(ws[i]->scales);
+    a.dstride[i] = ws[i]->expert_data_stride;
+    a.sstride[i] = ws[i]->expert_scale_stride;
+    a.g[i] = ws[i]->global_scale;
+  }
+  a.offsets = offsets;
+  a.y = ys;
+  a.E = (int)w->num_experts;
+  a.P = (int)rows;
+  a.n = (int)w->n;
+  a.k = (int)w->k;
+  kern<<<grid, kGgThreads, smem, st>>>(tx, a);
+  set_variant("%s_tc<fmt=%d,rows=128,tokens<=256,grid=%d>", SWI ? "grouped_swiglu" : "grouped_gemm", FMT, grid);
+  return launch_status();
+}
+
+template <int FMT>
+static qmm_status grouped_gemm_fmt(const qmm_weights* w, const qmm_weights* up, const uint16_t* xs,
+                                   const int32_t* offsets, int64_t rows, uint16_t* ys, cudaStream_t st,
+                                   const DevInfo* di) {
+  return up ? launch_grouped_gemm<FMT, true>(w, up, xs, offsets, rows, ys, st, di)
+            : launch_grouped_gemm<FMT, false>(w, nullptr, xs, offsets, rows, ys, st, di);
 }
 
 // ---------------------------------------------------------------------------
@@ -1472,11 +1520,21 @@ static qmm_status check_grouped_rows(const qmm_weights* w, const uint16_t* xs, c
   return QMM_OK;
 }
 
-// up: the second stack of the SwiGLU product, or null.
+// up: the second stack of the SwiGLU product, or null.  The tensor-core
+// kernel takes whole 128-wide k steps (the packed rows are then whole 8-byte
+// units in every format); the generic one the rest.
 static qmm_status grouped_rows(const qmm_weights* w, const qmm_weights* up, const uint16_t* xs,
                                const int32_t* offsets, int64_t rows, uint16_t* ys, cudaStream_t st,
                                const DevInfo* di) {
   qmm_status s;
+  if (w->k > 0 && w->k % 128 == 0) {
+    switch (w->fmt) {
+      case QMM_FMT_IQ4_NL: return grouped_gemm_fmt<1>(w, up, xs, offsets, rows, ys, st, di);
+      case QMM_FMT_FP4G16_F16: return grouped_gemm_fmt<2>(w, up, xs, offsets, rows, ys, st, di);
+      case QMM_FMT_MXFP4: return grouped_gemm_fmt<4>(w, up, xs, offsets, rows, ys, st, di);
+      default: return grouped_gemm_fmt<3>(w, up, xs, offsets, rows, ys, st, di);
+    }
+  }
   switch (w->fmt) {
     case QMM_FMT_IQ4_NL: s = launch_grouped<1>(w, xs, 1, 1, offsets, nullptr, ys, st, rows, up); break;
     case QMM_FMT_FP4G16_F16: s = launch_grouped<2>(w, xs, 1, 1, offsets, nullptr, ys, st, rows, up); break;

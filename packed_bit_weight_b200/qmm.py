@@ -111,8 +111,11 @@ def _check(status: int, where: str):
 
 
 def _stream(stream=None):
+    if stream is None and torch.cuda.is_initialized():
+        # the raw handle: building a Stream object costs more than the launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _need(t: torch.Tensor | None, nbytes: int, name: str) -> None:
@@ -389,10 +392,13 @@ def qmm_moe_routed(gate: PackedWeights, up: PackedWeights, down: PackedWeights, 
 def _here(t: torch.Tensor | None, esize: int | None, name: str):
     """_ptr for a tensor that must be on the current device (the C ABI
     launches there, whatever device the pointer is of)."""
-    p = _ptr(t, esize, name)
-    if t is not None and t.device.index != torch.cuda.current_device():
+    if t is None:
+        return None
+    if not (t.is_cuda and t.is_contiguous() and (esize is None or t.element_size() == esize)):
+        _ptr(t, esize, name)  # says what is wrong
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
-    return p
+    return t.data_ptr()
 
 
 def qmm_route_rows(topk_ids: torch.Tensor, num_experts: int, offsets: torch.Tensor, perm: torch.Tensor,
