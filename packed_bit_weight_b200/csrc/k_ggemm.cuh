@@ -12,17 +12,21 @@
 // 1,100 cycles of the 128-byte port for 512 cycles of MMA; with the weights
 // in TMEM the port carries X once in and once out and the lookups, ~650.
 //
-// Roles per CTA (persistent, one per SM):
+// Roles per CTA (persistent, one per SM, 24 warps):
 //   warp 0       X rows by TMA (64-row boxes, 128-byte swizzle), kGgStages deep
 //   warp 1       tcgen05.mma issue; owns the tensor memory
-//   warps 2-9    weight decode: packed chunks of 256 k arrive by cp.async in a
-//                ring, warps 2-5 decode the even 64-wide steps, 6-9 the odd
-//                ones (a thread then has two steps' time for one step's chain
-//                of wait, decode, tcgen05.st, fence, arrive)
-//   warps 10-13  epilogue: tcgen05.ld, fp16, store
+//   warps 2-3    packed weights by cp.async, chunks of 256 k, kGgSlots deep
+//   warps 4-19   weight decode: four groups of four warps, group j has step j
+//                of each chunk.  A step's chain (wait, read, look up, multiply,
+//                wait, tcgen05.st, arrive) is latency, ~1,000 cycles of it, and
+//                only more warps hide it
+//   warps 20-23  epilogue: tcgen05.ld, fp16, store
 // Tensor memory: kGgStages x 32 columns of weights and three accumulators of
-// 128 columns; a tile takes one accumulator per 128 rows, so the next tile
-// starts while the last one or two are still being stored.
+// 128 columns.  A tile of more than 128 rows takes the middle one and, in
+// turn, the first or the last, which are one run of columns (one MMA of N up
+// to 256 per k16 step); the epilogue drains the middle one first, so the next
+// tile waits for half of this one's stores.  Smaller tiles take the first and
+// the last in turn.
 //
 // SWI: the tile's 128 weight rows are 64 rows of gate and of up, 16 + 16 in
 // each warp's 32 lanes, so that SiLU(gate) * up needs one shuffle per pair of
@@ -37,13 +41,14 @@
 
 namespace qmm {
 
-constexpr int kGgStages = 4;
+constexpr int kGgStages = kGemmChunkSteps;        // stage = a step's place in its chunk
 constexpr int kGgSlots = 3;                       // packed chunks of 256 k in flight
 constexpr int kGgRows = 128;                      // weight rows per tile
 constexpr int kGgTok = 256;                       // rows of X per tile at most
 constexpr int kGgXBytes = kGgTok * kGemmBK * 2;   // 32 KB per stage
 constexpr int kGgMaxExperts = 256;
-constexpr int kGgThreads = (2 + kGemmDecodeWarps + 4) * 32;
+constexpr int kGgCopyWarps = 2, kGgGroups = 4, kGgDecodeWarps = 4 * kGgGroups;
+constexpr int kGgThreads = (2 + kGgCopyWarps + kGgDecodeWarps + 4) * 32;
 constexpr int kGgCodes = kGgRows * 128;           // FP4 slot: codes [128][128 B] (unit u of row r at u ^ (r & 7))
 constexpr int kGgSlotFp4 = kGgCodes + kGgRows * 32;   // then scales [128][32 B]
 constexpr int kGgSlotIq4 = 9 * kGgRows * 16;      // IQ4_NL slot: [9 units][128 rows][16 B]
@@ -80,6 +85,34 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// mbar_wait whose first polls touch nothing but the barrier (its time limit is
+// a global load and a timer read, which a wait of a few hundred cycles should
+// not pay for).
+__device__ __forceinline__ bool gg_wait(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; i++)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity);
+}
+
+// One arrival for a whole warp, once all its lanes are done (128 threads
+// arriving on one barrier one after another took longer than a k step).
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// True in one lane of the warp.  tcgen05.mma issued under it costs ~9 cycles,
+// under lane == 0 ~46 (the compiler cannot see that one lane is left).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// A value that is the same in every lane, as the compiler can see it.
+__device__ __forceinline__ uint32_t warp_uniform(uint32_t v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
+
 // Shared memory (from a 1,024-byte boundary): X stages, packed slots, the
 // IQ4_NL pair table (32 copies, one per bank), barriers.
 template <int FMT>
@@ -95,6 +128,126 @@ struct GgSmem {
 struct GgTile {
   int e, m0, cnt, n0;
 };
+
+// Step J (64 k) of tile row `row` from its packed chunk: 32 words of two
+// weights in k order, the exact decoded fp16 weights (E4M3: without the global
+// scale).  Rows past n decode to zeros.
+template <int FMT, int J>
+__device__ __forceinline__ void gg_decode(uint32_t src, int row, bool valid, uint32_t lut_lane, uint32_t (&o)[32]) {
+  if (FMT == 1) {
+    // two blocks: 36 bytes from byte 36 J of the row, in its units 2J .. 2J+2
+    uint32_t uw[12];
+#pragma unroll
+    for (int u = 0; u < 3; u++) {
+      const uint4 v = lds128(src + (2 * J + u) * (kGgRows * 16) + row * 16);
+      uw[4 * u] = v.x; uw[4 * u + 1] = v.y; uw[4 * u + 2] = v.z; uw[4 * u + 3] = v.w;
+    }
+    uint32_t qa[4], qb[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      qa[i] = __funnelshift_r(uw[J + i], uw[J + i + 1], 16);
+      qb[i] = uw[J + 5 + i];
+    }
+    uint32_t da = uw[J] & 0xFFFFu, db = uw[J + 4] >> 16;
+    da = valid ? (da | (da << 16)) : 0u;
+    db = valid ? (db | (db << 16)) : 0u;
+    uint32_t oa[16], ob[16];
+    iq4_block_chunks<7>(qa, da, lut_lane, oa);
+    iq4_block_chunks<7>(qb, db, lut_lane, ob);
+#pragma unroll
+    for (int i = 0; i < 16; i++) { o[i] = oa[i]; o[16 + i] = ob[i]; }
+  } else {
+    uint32_t q[8];
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      const uint4 v = lds128(src + row * 128 + (((2 * J + u) ^ (row & 7)) << 4));
+      q[4 * u] = v.x; q[4 * u + 1] = v.y; q[4 * u + 2] = v.z; q[4 * u + 3] = v.w;
+    }
+    uint32_t f1[4], f2[4];  // per 16 k: the scale, and for wide E8M0 scales a first factor
+    bool two = false;
+    if (FMT == 2) {
+      const uint2 sv = lds64(src + kGgCodes + row * 32 + (((J >> 1) ^ ((row >> 2) & 1)) << 4) + (J & 1) * 8);
+      f1[0] = bcast_lo(sv.x); f1[1] = bcast_hi(sv.x); f1[2] = bcast_lo(sv.y); f1[3] = bcast_hi(sv.y);
+    } else if (FMT == 3) {
+      const uint32_t sw = lds32(src + kGgCodes + row * 32 + J * 4);
+      const uint32_t e01 = e4m3x2_to_f16x2(sw & 0xFFFFu), e23 = e4m3x2_to_f16x2(sw >> 16);
+      f1[0] = bcast_lo(e01); f1[1] = bcast_hi(e01); f1[2] = bcast_lo(e23); f1[3] = bcast_hi(e23);
+    } else {
+      const uint32_t sw = lds32(src + kGgCodes + row * 32 + (J >> 1) * 4) >> ((J & 1) * 16);
+      const uint32_t b0 = sw & 0xFFu, b1 = (sw >> 8) & 0xFFu;
+      two = !(e8m0_f16_ok(b0) && e8m0_f16_ok(b1));
+      e8m0_f16_factors(b0, f2[0], f1[0]);
+      e8m0_f16_factors(b1, f2[2], f1[2]);
+      f1[1] = f1[0]; f1[3] = f1[2]; f2[1] = f2[0]; f2[3] = f2[2];
+    }
+    if (!valid) f1[0] = f1[1] = f1[2] = f1[3] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      uint32_t w4[4];
+      e2m1x8_to_f16x2(q[i], w4);
+      if (FMT == 4 && two) {
+#pragma unroll
+        for (int v = 0; v < 4; v++) w4[v] = hmul2(w4[v], f2[i >> 1]);
+      }
+#pragma unroll
+      for (int v = 0; v < 4; v++) o[4 * i + v] = hmul2(w4[v], f1[i >> 1]);
+    }
+    if (FMT == 4 && two && !valid) {  // (an infinite first product times 0)
+#pragma unroll
+      for (int i = 0; i < 32; i++) o[i] = 0u;
+    }
+  }
+}
+
+// SiLU(z) = z / (1 + e^-z) by the fast exponential and division: off by
+// 2 + 1.2 |z| and 2 fp32 steps, far below half an fp16 step of the result it
+// is rounded to.  (expf and the IEEE division, one warp per scheduler, took
+// longer than the tile's products: gate and up of 8,192 pairs 168 us.)
+__device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
+// Store 32 rows of a warp's columns.  p[i] holds two columns of one row, its
+// number's bits by exchange: bit 0 of the lane has been exchanged for the
+// lowest bit of i.  Two more steps (lane bits 1 and 2) leave 8 columns, 4 words,
+// of NR rows.  NR = 4: 32 columns, rows numbered 8i + (lane & 1) + (lane & 2) +
+// (lane & 4); NR = 2: 16 columns, rows 2 (8i + ...) + (lane >> 4).
+template <int NR>
+__device__ __forceinline__ void gg_store(const uint32_t (&p)[4 * NR], int lane, int left, uint16_t* y, int n, int col0,
+                                         bool vec) {
+  uint32_t q2[2 * NR][2];  // 4 columns
+#pragma unroll
+  for (int i = 0; i < 2 * NR; i++) {
+    const bool hi = lane & 2;
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, hi ? p[2 * i] : p[2 * i + 1], 2);
+    q2[i][0] = hi ? got : p[2 * i];
+    q2[i][1] = hi ? p[2 * i + 1] : got;
+  }
+  uint32_t q4[NR][4];  // 8 columns
+#pragma unroll
+  for (int i = 0; i < NR; i++) {
+    const bool hi = lane & 4;
+#pragma unroll
+    for (int w = 0; w < 2; w++) {
+      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, hi ? q2[2 * i][w] : q2[2 * i + 1][w], 4);
+      q4[i][w] = hi ? got : q2[2 * i][w];
+      q4[i][2 + w] = hi ? q2[2 * i + 1][w] : got;
+    }
+  }
+  const int col = col0 + (NR == 4 ? (lane & 24) : (lane & 8));
+#pragma unroll
+  for (int i = 0; i < NR; i++) {
+    const int r8 = 8 * i + (lane & 7);
+    const int row = NR == 4 ? r8 : 2 * r8 + (lane >> 4);
+    if (row >= left) continue;
+    uint16_t* yp = y + (int64_t)row * n + col;
+    if (vec && col + 8 <= n) {
+      *reinterpret_cast<uint4*>(yp) = make_uint4(q4[i][0], q4[i][1], q4[i][2], q4[i][3]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; c++)
+        if (col + c < n) yp[c] = (uint16_t)(q4[i][c >> 1] >> (16 * (c & 1)));
+    }
+  }
+}
 
 template <int FMT, bool SWI>
 __global__ void __launch_bounds__(kGgThreads, 1)
@@ -116,17 +269,17 @@ __global__ void __launch_bounds__(kGgThreads, 1)
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int s = 0; s < kGgStages; s++) {
-      mbar_init(full + 8 * s, 1 + 128);  // the X copies and one decode group
+      mbar_init(full + 8 * s, 1 + 4);  // the X copies and the four warps of a decode group
       mbar_init(empty + 8 * s, 1);       // MMA commit
     }
     for (int h = 0; h < 3; h++) {
       mbar_init(accf + 8 * h, 1);
-      mbar_init(acce + 8 * h, 128);
+      mbar_init(acce + 8 * h, 4);
     }
     mbar_init(done_bar, 1);
     for (int c = 0; c < kGgSlots; c++) {
-      mbar_init(cfull + 8 * c, kGemmDecodeThreads);
-      mbar_init(cempty + 8 * c, kGemmDecodeThreads);
+      mbar_init(cfull + 8 * c, kGgCopyWarps * 32);  // every copying thread's copies landed
+      mbar_init(cempty + 8 * c, kGgDecodeWarps);
     }
     fence_mbar_init();
   }
@@ -172,6 +325,12 @@ __global__ void __launch_bounds__(kGgThreads, 1)
   const int G = (int)gridDim.x;
   const int my_tiles = (tiles - (int)blockIdx.x + G - 1) / G;  // (0 for CTAs past the last tile)
   const int ksteps = k / kGemmBK;
+  const int nck = (ksteps + kGemmChunkSteps - 1) / kGemmChunkSteps;  // chunks per tile (the last may be half)
+  const int nfull = ksteps / kGemmChunkSteps;
+  // A step's stage is its place in its chunk, so that a stage always belongs to
+  // one decode group (half chunks leave stages 2 and 3 out): the how-manieth
+  // use of its stage step ks of the li-th tile is.
+  auto stage_use = [&](int li, int ks) { return (uint32_t)(li * ((ks & 3) < 2 ? nck : nfull) + (ks >> 2)); };
 
   auto tile_at = [&](int li) {
     const int tile = (int)blockIdx.x + li * G;
@@ -198,287 +357,244 @@ __global__ void __launch_bounds__(kGgThreads, 1)
     // ------------------------------ X rows ---------------------------------
     if (lane == 0) {
       prefetch_tmap(&tm_x);
-      int gs = 0, issued = 0;
+      uint32_t any = 0, par = 0;  // per stage: copies issued, parity of the last use
       const int tissue = (g_test_flags & kTestWithholdXTiles) ? 0 : my_tiles;  // test switch: issue nothing
       for (int li = 0; li < tissue && !s_abort; li++) {
         const GgTile t = tile_at(li);
         const int boxes = (t.cnt + 63) >> 6;
-        for (int ks = 0; ks < ksteps; ks++, gs++) {
-          const int s = gs % kGgStages;
-          if (s_abort || !mbar_wait(empty + 8 * s, ((uint32_t)(gs / kGgStages) & 1u) ^ 1u)) { s_abort = 1; break; }
+        for (int ks = 0; ks < ksteps; ks++) {
+          const uint32_t s = ks & 3, use = stage_use(li, ks);
+          if (!gg_wait(empty + 8 * s, (use & 1u) ^ 1u)) { s_abort = 1; break; }
           mbar_arrive_expect_tx(full + 8 * s, (uint32_t)boxes * 64u * 128u);
           for (int b = 0; b < boxes; b++)
             tma_load_2d(x_s + s * kGgXBytes + b * 64 * 128, &tm_x, ks * kGemmBK, t.m0 + 64 * b, full + 8 * s);
-          issued = gs + 1;
+          any |= 1u << s;
+          par = (par & ~(1u << s)) | ((use & 1u) << s);
         }
       }
-      for (int s = 0; s < kGgStages && s < issued; s++) {  // drain our copies
-        const int last = issued - 1 - ((issued - 1 - s) % kGgStages);
-        mbar_wait(full + 8 * s, (uint32_t)(last / kGgStages) & 1u);
-      }
+      for (uint32_t s = 0; s < kGgStages; s++)  // drain our copies
+        if (any >> s & 1u) gg_wait(full + 8 * s, par >> s & 1u);
     }
   } else if (warp == 1) {
     // ---------------------------- MMA issuer ------------------------------
-    if (lane == 0) {
-      int gs = 0, hc = 0;  // k steps, accumulators so far
-      for (int li = 0; li < my_tiles && !s_abort; li++) {
-        const GgTile t = tile_at(li);
-        const int halves = t.cnt > 128 ? 2 : 1;
-        bool ok = true;
-        for (int h = 0; h < halves; h++)
-          ok = ok && mbar_wait(acce + 8 * ((hc + h) % 3), ((uint32_t)((hc + h) / 3) & 1u) ^ 1u);
-        if (!ok) { s_abort = 1; break; }
+    // The whole warp walks the loop and one lane issues: with everything an MMA
+    // names computed alike in all lanes (warp_uniform: a warp reduction, whose
+    // result is a uniform register) no operand has to be moved there per MMA.
+    const uint32_t d0 = warp_uniform(tmem) + kGgAccCol, a0 = warp_uniform(tmem) + kGgACol;
+    const uint32_t xb = warp_uniform(x_s), fb = warp_uniform(full), eb = warp_uniform(empty);
+    const bool leader = elect_one();
+    uint32_t used[3] = {0, 0, 0};  // tiles so far per accumulator
+    for (int li = 0; li < my_tiles; li++) {
+      const int cnt = (int)warp_uniform((uint32_t)tile_at(li).cnt);
+      const int own = (li & 1) ? 2 : 0;  // the accumulator that is not shared with the next tile
+      const bool big = cnt > 128;
+      bool ok = !s_abort && gg_wait(acce + 8 * own, (used[own == 0 ? 0 : 2] & 1u) ^ 1u);
+      if (big) ok = ok && gg_wait(acce + 8, (used[1] & 1u) ^ 1u);
+      if (!__all_sync(0xFFFFFFFFu, ok)) { s_abort = 1; break; }
+      if (own == 0) used[0]++;
+      else used[2]++;
+      if (big) used[1]++;
+      tc_fence_after();
+      const uint32_t d = d0 + (own == 0 ? 0u : big ? 128u : 256u);
+      const uint32_t idesc = umma_idesc_f16((cnt + 15) & ~15);
+      for (int ks = 0; ks < ksteps; ks++) {
+        const uint32_t s = ks & 3;
+        ok = gg_wait(fb + 8 * s, stage_use(li, ks) & 1u);
+        if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; s_abort = 1; break; }
         tc_fence_after();
-        uint32_t d[2], idesc[2];
+        const uint64_t db = umma_desc_k128(xb + s * kGgXBytes);
+        const uint32_t wa = a0 + 32u * s;
+        if (leader) {
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          d[h] = tmem + kGgAccCol + 128u * (uint32_t)((hc + h) % 3);
-          const int c = min(128, t.cnt - 128 * h);
-          idesc[h] = umma_idesc_f16((c + 15) & ~15);
+          for (int kk = 0; kk < kGemmBK / 16; kk++)
+            umma_f16_ta(d, wa + 8u * kk, db + (uint64_t)(2 * kk), idesc, (ks | kk) != 0);
+          umma_commit(eb + 8 * s);
         }
-        for (int ks = 0; ks < ksteps; ks++, gs++) {
-          const int s = gs % kGgStages;
-          if (s_abort || !mbar_wait(full + 8 * s, (uint32_t)(gs / kGgStages) & 1u)) { s_abort = 1; ok = false; break; }
-          tc_fence_after();
-          const uint64_t db = umma_desc_k128(x_s + s * kGgXBytes);
-          const uint32_t wa = tmem + kGgACol + 32u * (uint32_t)s;
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            if (h < halves) {
-#pragma unroll
-              for (int kk = 0; kk < kGemmBK / 16; kk++)
-                umma_f16_ta(d[h], wa + 8u * kk, db + (uint64_t)(h * (128 * 128 / 16) + 2 * kk), idesc[h], (ks | kk) != 0);
-            }
-          }
-          umma_commit(empty + 8 * s);
-        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (leader) {
+        umma_commit(accf + 8 * own);
+        if (big) umma_commit(accf + 8);
+      }
+      __syncwarp();
+    }
+    if (leader) umma_commit(done_bar);  // every MMA we issued has completed when this arrives
+  } else if (warp < 2 + kGgCopyWarps) {
+    // --------------------------- packed weights ----------------------------
+    // Warp cw copies the tile's rows 64 cw .. 64 cw + 63.  IQ4_NL rows are
+    // copied in units of 8 bytes (a row of k % 256 = 128 starts on 8), 18 a
+    // chunk: 16 lanes take the first 16 of a row, and the rest follow by twos;
+    // FP4 rows in 8 units of 16 bytes.  Rows past n copy row n - 1.
+    const int cw = warp - 2;
+    const int rowb = FMT == 1 ? (k >> 5) * 18 : k >> 1;
+    constexpr int kScaleHalf = FMT == 2 ? 16 : FMT == 3 ? 8 : 4;  // scale bytes of 128 k
+    const int srow = (k >> 7) * kScaleHalf;
+    constexpr int kPer = FMT == 1 ? 2 : 4, kLanes = 32 / kPer;  // rows per instruction, lanes per row
+    const int lr = lane / kLanes, u = lane % kLanes;
+    // tile row 64 cw + i (i < 64, its low part may depend on the lane) as a
+    // weight row; its stack with SWI is (i >> 4) & 1
+    auto wrow = [&](int n0, int i) { return min(SWI ? n0 + 32 * cw + ((i >> 5) << 4) + (i & 15) : n0 + 64 * cw + i, n - 1); };
+    int ck = 0;  // chunks so far
+    bool ok = true;
+    for (int li = 0; li < my_tiles && ok; li++) {
+      const GgTile g = tile_at(li);
+      const uint8_t* b0 = a.data[0] + g.e * a.dstride[0];
+      const uint8_t* b1 = SWI ? a.data[1] + g.e * a.dstride[1] : b0;
+      const uint8_t* s0 = FMT != 1 ? a.scales[0] + g.e * a.sstride[0] : nullptr;
+      const uint8_t* s1 = FMT != 1 && SWI ? a.scales[1] + g.e * a.sstride[1] : s0;
+      for (int cc = 0; cc < nck; cc++, ck++) {
+        const int slot = ck % kGgSlots;
+        ok = gg_wait(cempty + 8 * slot, ((uint32_t)(ck / kGgSlots) & 1u) ^ 1u);
         if (!ok) break;
-        for (int h = 0; h < halves; h++) umma_commit(accf + 8 * ((hc + h) % 3));
-        hc += halves;
-      }
-      umma_commit(done_bar);  // every MMA we issued has completed when this arrives
-    }
-  } else if (warp < 2 + kGemmDecodeWarps) {
-    // --------------------------- weight decode -----------------------------
-    const int t = threadIdx.x - 64;
-    const int group = t >> 7;                 // decodes the steps of this parity
-    const int row = ((warp & 3) << 5) | lane; // tile row = TMEM lane (a warp reaches lanes 32 (warp % 4) .. + 31)
-    const int nck = (ksteps + kGemmChunkSteps - 1) / kGemmChunkSteps;  // chunks per tile (the last may be half)
-    const int total_ck = my_tiles * nck;
-    // source row of tile row r: the stack and the weight row (clamped to n-1)
-    auto row_of = [&](const GgTile& g, int r, int& which) {
-      int w = g.n0 + r;
-      which = 0;
-      if (SWI) {
-        which = (r >> 4) & 1;
-        w = g.n0 + ((r >> 5) << 4) + (r & 15);
-      }
-      return w;
-    };
-    GgTile gi = {}, gd = {};  // the tiles of the chunk being copied and of the one being decoded
-    auto issue_chunk = [&](int c) -> bool {
-      const int slot = c % kGgSlots;
-      if (!mbar_wait(cempty + 8 * slot, ((uint32_t)(c / kGgSlots) & 1u) ^ 1u)) return false;
-      if (c % nck == 0) gi = tile_at(c / nck);
-      const GgTile& g = gi;
-      const int kc = (c % nck) * (kGemmChunkSteps * kGemmBK);
-      const bool whole = k - kc >= kGemmChunkSteps * kGemmBK;  // 256 k, else 128
-      const uint32_t dst = p_s + slot * SM::kSlot;
-      if (FMT == 1) {  // 18-byte blocks: 144 (72) bytes a row; rows start on 8 bytes at least
-        const int64_t rowb = (int64_t)(k >> 5) * 18;
-        const int64_t off = (int64_t)(kc >> 5) * 18;
-        if ((k & 255) == 0) {
+        const bool whole = k - cc * 256 >= 256;  // 256 k, else the last 128
+        const uint32_t dst = p_s + slot * SM::kSlot + (uint32_t)(cw * 64) * (FMT == 1 ? 16u : 128u);
+        const int off = cc * (FMT == 1 ? 144 : 128);
+        // blocks of 16 rows, one stack each
 #pragma unroll
-          for (int i = 0; i < (9 * kGgRows + kGemmDecodeThreads - 1) / kGemmDecodeThreads; i++) {
-            const int pc = i * kGemmDecodeThreads + t;
-            if (pc >= 9 * kGgRows) break;
-            const int r = pc / 9, u = pc - r * 9;
-            int which;
-            const int64_t w = min(row_of(g, r, which), n - 1);
-            cp_async16_g(dst + u * (kGgRows * 16) + r * 16, a.data[which] + g.e * a.dstride[which] + w * rowb + off + u * 16);
-          }
-        } else {
-          const int units = whole ? 18 : 9;  // of 8 bytes
-          for (int pc = t; pc < units * kGgRows; pc += kGemmDecodeThreads) {
-            const int r = pc / units, u = pc - r * units;
-            int which;
-            const int64_t w = min(row_of(g, r, which), n - 1);
-            cp_async8_g(dst + (u >> 1) * (kGgRows * 16) + r * 16 + (u & 1) * 8,
-                        a.data[which] + g.e * a.dstride[which] + w * rowb + off + u * 8);
-          }
-        }
-      } else {
-        const int units = whole ? 8 : 4, sh = whole ? 3 : 2;  // codes: 16-byte units of a row
-        for (int pc = t; pc < units * kGgRows; pc += kGemmDecodeThreads) {
-          const int r = pc >> sh, u = pc & (units - 1);
-          int which;
-          const int64_t w = min(row_of(g, r, which), n - 1);
-          cp_async16_g(dst + r * 128 + ((u ^ (r & 7)) << 4),
-                       a.data[which] + g.e * a.dstride[which] + w * (int64_t)(k >> 1) + (kc >> 1) + u * 16);
-        }
-        // scales: two halves of 128 k a row, of 16 (fp16), 8 (E4M3) or 4 bytes (E8M0)
-        const int r = t >> 1, h = t & 1;
-        if (whole || h == 0) {
-          int which;
-          const int64_t w = min(row_of(g, r, which), n - 1);
-          const uint8_t* sp = a.scales[which] + g.e * a.sstride[which];
-          const uint32_t sd = dst + kGgCodes + r * 32;
-          if (FMT == 2)
-            cp_async16_g(sd + ((h ^ ((r >> 2) & 1)) << 4), sp + (w * (int64_t)(k >> 4) + (kc >> 4)) * 2 + h * 16);
-          else if (FMT == 3)
-            cp_async8_g(sd + h * 8, sp + w * (int64_t)(k >> 4) + (kc >> 4) + h * 8);
-          else
-            cp_async4_g(sd + h * 4, sp + w * (int64_t)(k >> 5) + (kc >> 5) + h * 4);
-        }
-      }
-      cp_async_mbar_arrive_noinc(cfull + 8 * slot);
-      return true;
-    };
-    bool stop = false;
-    for (int c = 0; c < kGgSlots - 1 && c < total_ck && !stop; c++) stop = !issue_chunk(c);
-    int step0 = 0;  // global step number of the chunk's first step
-    for (int c = 0; c < total_ck && !stop; c++) {
-      if (c + kGgSlots - 1 < total_ck && !issue_chunk(c + kGgSlots - 1)) { s_abort = 1; break; }
-      const int slot = c % kGgSlots;
-      if (s_abort || !mbar_wait(cfull + 8 * slot, (uint32_t)(c / kGgSlots) & 1u)) { s_abort = 1; break; }
-      if (c % nck == 0) gd = tile_at(c / nck);
-      int which;
-      const bool valid = row_of(gd, row, which) < n;
-      const int steps = min(kGemmChunkSteps, ksteps - (c % nck) * kGemmChunkSteps);
-      const uint32_t src = p_s + slot * SM::kSlot;
+        for (int q = 0; q < 4; q++) {
+          const uint8_t* src = ((q & 1) ? b1 : b0) + off;
+          if (FMT == 1) {
+            if (whole || u < 9) {
 #pragma unroll
-      for (int j = 0; j < kGemmChunkSteps; j++) {
-        if (j >= steps) break;
-        const int gs = step0 + j;
-        if ((gs & 1) != group) continue;
-        uint32_t o[32];  // the step's 64 weights of this row, two per word, k order
-        if (FMT == 1) {
-          // two blocks: 36 bytes from byte 36j of the row, in its units 2j .. 2j+2
-          uint32_t uw[12];
-#pragma unroll
-          for (int u = 0; u < 3; u++) {
-            const uint4 v = lds128(src + (2 * j + u) * (kGgRows * 16) + row * 16);
-            uw[4 * u] = v.x; uw[4 * u + 1] = v.y; uw[4 * u + 2] = v.z; uw[4 * u + 3] = v.w;
-          }
-          uint32_t w[9];
-#pragma unroll
-          for (int i = 0; i < 9; i++) w[i] = uw[i + j];  // (j is a constant: the loop is unrolled)
-          uint32_t qa[4], qb[4];
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            qa[i] = __funnelshift_r(w[i], w[i + 1], 16);
-            qb[i] = w[5 + i];
-          }
-          uint32_t da = w[0] & 0xFFFFu, db = w[4] >> 16;
-          da = valid ? (da | (da << 16)) : 0u;
-          db = valid ? (db | (db << 16)) : 0u;
-          const uint32_t lut_lane = lut_s + 4u * (uint32_t)lane;
-          uint32_t oa[16], ob[16];
-          iq4_block_chunks<7>(qa, da, lut_lane, oa);
-          iq4_block_chunks<7>(qb, db, lut_lane, ob);
-#pragma unroll
-          for (int i = 0; i < 16; i++) { o[i] = oa[i]; o[16 + i] = ob[i]; }
-        } else {
-          uint32_t q[8];
-#pragma unroll
-          for (int u = 0; u < 2; u++) {
-            const uint4 v = lds128(src + row * 128 + (((2 * j + u) ^ (row & 7)) << 4));
-            q[4 * u] = v.x; q[4 * u + 1] = v.y; q[4 * u + 2] = v.z; q[4 * u + 3] = v.w;
-          }
-          uint32_t f1[4], f2[4];  // per 16 k: the scale, and for wide E8M0 scales a second factor
-          bool two = false;
-          if (FMT == 2) {
-            const uint2 sv = lds64(src + kGgCodes + row * 32 + (((j >> 1) ^ ((row >> 2) & 1)) << 4) + (j & 1) * 8);
-            f1[0] = bcast_lo(sv.x); f1[1] = bcast_hi(sv.x); f1[2] = bcast_lo(sv.y); f1[3] = bcast_hi(sv.y);
-          } else if (FMT == 3) {
-            const uint32_t sw = lds32(src + kGgCodes + row * 32 + j * 4);
-            const uint32_t e01 = e4m3x2_to_f16x2(sw & 0xFFFFu), e23 = e4m3x2_to_f16x2(sw >> 16);
-            f1[0] = bcast_lo(e01); f1[1] = bcast_hi(e01); f1[2] = bcast_lo(e23); f1[3] = bcast_hi(e23);
-          } else {
-            const uint32_t sw = lds32(src + kGgCodes + row * 32 + (j >> 1) * 4) >> ((j & 1) * 16);
-            const uint32_t b0 = sw & 0xFFu, b1 = (sw >> 8) & 0xFFu;
-            two = !(e8m0_f16_ok(b0) && e8m0_f16_ok(b1));
-            e8m0_f16_factors(b0, f2[0], f1[0]);
-            e8m0_f16_factors(b1, f2[2], f1[2]);
-            f1[1] = f1[0]; f1[3] = f1[2]; f2[1] = f2[0]; f2[3] = f2[2];
-          }
-          if (!valid) f1[0] = f1[1] = f1[2] = f1[3] = 0u;
-#pragma unroll
-          for (int i = 0; i < 8; i++) {
-            uint32_t w4[4];
-            e2m1x8_to_f16x2(q[i], w4);
-            if (FMT == 4 && two) {
-#pragma unroll
-              for (int v = 0; v < 4; v++) w4[v] = hmul2(w4[v], f2[i >> 1]);
+              for (int i = 0; i < 8; i++)
+                cp_async8_g(dst + (u >> 1) * (kGgRows * 16) + (16 * q + 2 * i + lr) * 16 + (u & 1) * 8,
+                            src + (int64_t)wrow(g.n0, 16 * q + 2 * i + lr) * rowb + u * 8);
             }
+            if (whole)
+              cp_async8_g(dst + 8 * (kGgRows * 16) + (16 * q + (lane >> 1)) * 16 + (lane & 1) * 8,
+                          src + (int64_t)wrow(g.n0, 16 * q + (lane >> 1)) * rowb + 128 + (lane & 1) * 8);
+          } else {
+            if (whole || u < 4) {
 #pragma unroll
-            for (int v = 0; v < 4; v++) o[4 * i + v] = hmul2(w4[v], f1[i >> 1]);
-          }
-          if (FMT == 4 && two && !valid) {  // (an infinite first product times 0)
-#pragma unroll
-            for (int i = 0; i < 32; i++) o[i] = 0u;
+              for (int i = 0; i < 4; i++) {
+                const int r = 16 * q + 4 * i + lr;
+                cp_async16_g(dst + r * 128 + ((u ^ (r & 7)) << 4), src + (int64_t)wrow(g.n0, r) * rowb + u * 16);
+              }
+            }
+            const int h = lane & 1;  // scales: two halves of 128 k a row
+            if (whole || h == 0) {
+              const int r = 16 * q + (lane >> 1);
+              const uint8_t* sp = ((q & 1) ? s1 : s0) + (int64_t)wrow(g.n0, r) * srow + (cc * 2 + h) * kScaleHalf;
+              const uint32_t sd = p_s + slot * SM::kSlot + kGgCodes + (cw * 64 + r) * 32;
+              if (FMT == 2) cp_async16_g(sd + ((h ^ ((r >> 2) & 1)) << 4), sp);
+              else if (FMT == 3) cp_async8_g(sd + h * 8, sp);
+              else cp_async4_g(sd + h * 4, sp);
+            }
           }
         }
-        const int s = gs % kGgStages;
-        const bool ok = !s_abort && mbar_wait(empty + 8 * s, ((uint32_t)(gs / kGgStages) & 1u) ^ 1u);
-        if (!__all_sync(0xFFFFFFFFu, ok)) { s_abort = 1; stop = true; break; }  // (the stores are warp-wide)
-        tc_fence_after();
-        tmem_st32(tmem + kGgACol + 32u * (uint32_t)s + ((uint32_t)((warp & 3) * 32) << 16), o);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(full + 8 * s);
+        cp_async_mbar_arrive_noinc(cfull + 8 * slot);
       }
-      step0 += steps;
-      mbar_arrive(cempty + 8 * slot);
     }
+    if (!ok) s_abort = 1;
     asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp < 2 + kGgCopyWarps + kGgDecodeWarps) {
+    // --------------------------- weight decode -----------------------------
+    const int group = (warp - 2 - kGgCopyWarps) >> 2;  // its step of every chunk
+    const int row = ((warp & 3) << 5) | lane;  // tile row = TMEM lane (a warp reaches lanes 32 (warp % 4) .. + 31)
+    const uint32_t lane_tm = tmem + kGgACol + ((uint32_t)((warp & 3) * 32) << 16);
+    int ck = 0;  // chunks so far
+    bool ok = true;
+    for (int li = 0; li < my_tiles && ok; li++) {
+      const int n0 = tile_at(li).n0;
+      const bool valid = (SWI ? n0 + ((row >> 5) << 4) + (row & 15) : n0 + row) < n;
+      for (int cc = 0; cc < nck; cc++, ck++) {
+        const int slot = ck % kGgSlots;
+        ok = gg_wait(cfull + 8 * slot, (uint32_t)(ck / kGgSlots) & 1u);
+        if (!ok) break;
+        const int steps = min(kGemmChunkSteps, ksteps - cc * kGemmChunkSteps);
+        if (group < steps) {
+          const uint32_t src = p_s + slot * SM::kSlot;
+          uint32_t o[32];  // the step's 64 weights of this row, two per word, k order
+          const uint32_t lut_lane = lut_s + 4u * (uint32_t)lane;
+          if (group == 0) gg_decode<FMT, 0>(src, row, valid, lut_lane, o);
+          else if (group == 1) gg_decode<FMT, 1>(src, row, valid, lut_lane, o);
+          else if (group == 2) gg_decode<FMT, 2>(src, row, valid, lut_lane, o);
+          else gg_decode<FMT, 3>(src, row, valid, lut_lane, o);
+          const int s = group;
+          ok = gg_wait(empty + 8 * s, (stage_use(li, cc * kGemmChunkSteps + group) & 1u) ^ 1u);
+          ok = __all_sync(0xFFFFFFFFu, ok);  // (the stores are warp-wide)
+          if (!ok) break;
+          tc_fence_after();
+          tmem_st32(lane_tm + 32u * (uint32_t)s, o);
+          tmem_st_wait();
+          tc_fence_before();
+          warp_arrive(full + 8 * s, lane);
+        }
+        warp_arrive(cempty + 8 * slot, lane);
+      }
+    }
+    if (!ok) s_abort = 1;
   } else {
     // ------------------------------ epilogue ------------------------------
+    // A lane holds one output column of 32 rows; lanes exchange (3 butterfly
+    // steps) until each holds 8 columns of 4 rows (SWI: of 2), which is one
+    // 16-byte store a row where the rows of y are 16-byte aligned.
     const int q = warp & 3;  // TMEM lanes 32q ..
     const float g0 = (FMT == 3) ? a.g[0] : 1.0f, g1 = (FMT == 3) ? a.g[1] : 1.0f;
-    int hc = 0;
+    const bool vec = (n & 7) == 0;
+    uint32_t used[3] = {0, 0, 0};
     for (int li = 0; li < my_tiles; li++) {
       const GgTile t = tile_at(li);
-      const int halves = t.cnt > 128 ? 2 : 1;
-      const int col = SWI ? t.n0 + 16 * q + (lane & 15) : t.n0 + 32 * q + lane;  // this lane's output column
+      const int own = (li & 1) ? 2 : 0;
+      const bool big = t.cnt > 128;
+      const int col0 = SWI ? t.n0 + 16 * q : t.n0 + 32 * q;  // this warp's first output column
       bool ok = true;
-      for (int h = 0; h < halves; h++, hc++) {
-        const int acc = hc % 3;
-        ok = !s_abort && mbar_wait(accf + 8 * acc, (uint32_t)(hc / 3) & 1u);
+      for (int h = 0; h < (big ? 2 : 1); h++) {
+        const int acc = (big && h == 0) ? 1 : own;             // the middle accumulator first
+        const int first = (big && (acc == 1) == (own == 0)) ? 128 : 0;  // the tile's row in its column 0
+        const uint32_t turn = acc == 0 ? used[0]++ : acc == 1 ? used[1]++ : used[2]++;
+        ok = gg_wait(accf + 8 * acc, turn & 1u);
         if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
         tc_fence_after();
-        const int c = min(128, t.cnt - 128 * h);
+        const int c = min(128, t.cnt - first);
         for (int j = 0; j < c; j += 32) {
           uint32_t r[32];
           tmem_ld32(tmem + kGgAccCol + 128u * acc + (uint32_t)j + ((uint32_t)(32 * q) << 16), r);
           tmem_ld_wait();
-          const int64_t m = t.m0 + 128 * h + j;
-          uint16_t* yp = a.y + m * n + col;
+          const int64_t m = t.m0 + first + j;
           const int left = c - j;
           if (!SWI) {
+            uint32_t p[16];  // after the exchange over lane bit 0: columns (lane & ~1, + 1) of row 2i + (lane & 1)
 #pragma unroll
-            for (int i = 0; i < 32; i++)
-              if (i < left && col < n) yp[(int64_t)i * n] = f32_to_f16_bits(__uint_as_float(r[i]) * g0);
+            for (int i = 0; i < 16; i++) {
+              const bool odd = lane & 1;
+              const float mine = __uint_as_float(odd ? r[2 * i + 1] : r[2 * i]) * g0;
+              const float other =
+                  __uint_as_float(__shfl_xor_sync(0xFFFFFFFFu, odd ? r[2 * i] : r[2 * i + 1], 1)) * g0;
+              p[i] = odd ? f32x2_to_f16x2(other, mine) : f32x2_to_f16x2(mine, other);
+            }
+            gg_store<4>(p, lane, left, a.y + m * n, n, col0, vec);
           } else {
             const bool up = (lane & 16) != 0;  // lanes 0-15 hold gate rows, 16-31 the same rows of up
+            float v[16];  // row 2i + (lane >> 4) of column lane & 15
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {  // gate lanes take token i, up lanes token i + 1
-              const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? r[i] : r[i + 1], 16);
-              const float zg = __uint_as_float(up ? got : r[i]) * g0, zu = __uint_as_float(up ? r[i + 1] : got) * g1;
-              const int tok = i + (up ? 1 : 0);
-              if (tok < left && col < n) yp[(int64_t)tok * n] = f32_to_f16_bits(zg / (1.0f + expf(-zg)) * zu);
+            for (int i = 0; i < 16; i++) {
+              const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? r[2 * i] : r[2 * i + 1], 16);
+              const float zg = __uint_as_float(up ? got : r[2 * i]) * g0;
+              const float zu = __uint_as_float(up ? r[2 * i + 1] : got) * g1;
+              v[i] = silu_fast(zg) * zu;
             }
+            uint32_t p[8];  // columns (lane & 14, + 1) of row 2 (2i + (lane & 1)) + (lane >> 4)
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+              const bool odd = lane & 1;
+              const float mine = odd ? v[2 * i + 1] : v[2 * i];
+              const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[2 * i] : v[2 * i + 1], 1);
+              p[i] = odd ? f32x2_to_f16x2(other, mine) : f32x2_to_f16x2(mine, other);
+            }
+            gg_store<2>(p, lane, left, a.y + m * n, n, col0, vec);
           }
         }
         tc_fence_before();
-        mbar_arrive(acce + 8 * acc);
+        warp_arrive(acce + 8 * acc, lane);
       }
       if (!ok) { s_abort = 1; break; }
     }
   }
 
   // teardown: no MMA of ours may still be using tensor memory
-  if (warp == 1 && lane == 0) mbar_wait(done_bar, 0);
+  if (warp == 1 && lane == 0) gg_wait(done_bar, 0);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -65,15 +65,15 @@ def product_bound(y, a, k):
 
 def swiglu_bound(zg, ag, zu, au, k):
     """(h, bound): h = SiLU(zg) zu.  Both sums are off by at most d =
-    2 U32 (k + 2) sum |w x|; |SiLU'| <= 1.1; exp, the sum, the division and the
-    product are off by at most 16 U32 together."""
+    2 U32 (k + 2) sum |w x|, and |SiLU'| <= 1.1.  The fast exponential is off by
+    2 + 1.173 |z| steps (2 U32 each), the fast division by 2, the sum and the
+    product by half a step: (4 + 2.35 |z| + 4 + 2) U32 together."""
     dg, du = 2 * U32 * (k + 2) * ag, 2 * U32 * (k + 2) * au
     with np.errstate(over="ignore"):
         s = zg / (1.0 + np.exp(-zg))
     h = s * zu
     err = 1.1 * dg * np.abs(zu) + np.abs(s) * du + 1.1 * dg * du
-    # SiLU of a very negative z is z e^z: exp(-z) is off by 2^-23 |z| relative where z itself is rounded
-    rel = 16 * U32 + 2 * U32 * np.abs(zg)
+    rel = (10 + 2.35 * np.abs(zg)) * U32
     err = err + rel * np.abs(h)
     return h, err + U16 * (np.abs(h) + err) + T16
 
