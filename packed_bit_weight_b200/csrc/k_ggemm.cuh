@@ -51,7 +51,7 @@ constexpr int kGgCopyWarps = 2, kGgGroups = 4, kGgDecodeWarps = 4 * kGgGroups;
 constexpr int kGgThreads = (2 + kGgCopyWarps + kGgDecodeWarps + 4) * 32;
 constexpr int kGgCodes = kGgRows * 128;           // FP4 slot: codes [128][128 B] (unit u of row r at u ^ (r & 7))
 constexpr int kGgSlotFp4 = kGgCodes + kGgRows * 32;   // then scales [128][32 B]
-constexpr int kGgSlotIq4 = 9 * kGgRows * 16;      // IQ4_NL slot: [9 units][128 rows][16 B]
+constexpr int kGgSlotIq4 = kGgRows * 144;         // IQ4_NL slot: [128 rows][144 B] (9 units: 16-byte reads of 8 rows hit 8 bank groups)
 constexpr uint32_t kGgAccCol = 0, kGgACol = 384;  // TMEM columns: 3 x 128 accumulators, 4 x 32 weights
 
 struct GgArgs {
@@ -139,23 +139,24 @@ __device__ __forceinline__ void gg_decode(uint32_t src, int row, bool valid, uin
     uint32_t uw[12];
 #pragma unroll
     for (int u = 0; u < 3; u++) {
-      const uint4 v = lds128(src + (2 * J + u) * (kGgRows * 16) + row * 16);
+      const uint4 v = lds128(src + row * 144 + (2 * J + u) * 16);
       uw[4 * u] = v.x; uw[4 * u + 1] = v.y; uw[4 * u + 2] = v.z; uw[4 * u + 3] = v.w;
     }
-    uint32_t qa[4], qb[4];
+    const uint32_t da = __byte_perm(uw[J], 0u, valid ? 0x1010u : 0x4444u);
+    const uint32_t db = __byte_perm(uw[J + 4], 0u, valid ? 0x3232u : 0x4444u);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      qa[i] = __funnelshift_r(uw[J + i], uw[J + i + 1], 16);
-      qb[i] = uw[J + 5 + i];
+    for (int i = 0; i < 8; i++) {  // index words: 4 of each block
+      const uint32_t q = i < 4 ? __funnelshift_r(uw[J + i], uw[J + i + 1], 16) : uw[J + 1 + i];
+      const uint32_t d = i < 4 ? da : db;
+      uint32_t w[4];  // byte b: weights (4i + b, 4i + b + 16) of the block
+#pragma unroll
+      for (int b = 0; b < 4; b++) w[b] = hmul2(lds32(lut_addr(q, b, lut_lane)), d);
+      const int at = (i >> 2) * 16 + (i & 3) * 2;
+      o[at] = __byte_perm(w[0], w[1], 0x5410);
+      o[at + 1] = __byte_perm(w[2], w[3], 0x5410);
+      o[at + 8] = __byte_perm(w[0], w[1], 0x7632);
+      o[at + 9] = __byte_perm(w[2], w[3], 0x7632);
     }
-    uint32_t da = uw[J] & 0xFFFFu, db = uw[J + 4] >> 16;
-    da = valid ? (da | (da << 16)) : 0u;
-    db = valid ? (db | (db << 16)) : 0u;
-    uint32_t oa[16], ob[16];
-    iq4_block_chunks<7>(qa, da, lut_lane, oa);
-    iq4_block_chunks<7>(qb, db, lut_lane, ob);
-#pragma unroll
-    for (int i = 0; i < 16; i++) { o[i] = oa[i]; o[16 + i] = ob[i]; }
   } else {
     uint32_t q[8];
 #pragma unroll
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kGgThreads, 1)
         ok = gg_wait(cempty + 8 * slot, ((uint32_t)(ck / kGgSlots) & 1u) ^ 1u);
         if (!ok) break;
         const bool whole = k - cc * 256 >= 256;  // 256 k, else the last 128
-        const uint32_t dst = p_s + slot * SM::kSlot + (uint32_t)(cw * 64) * (FMT == 1 ? 16u : 128u);
+        const uint32_t dst = p_s + slot * SM::kSlot + (uint32_t)(cw * 64) * (FMT == 1 ? 144u : 128u);
         const int off = cc * (FMT == 1 ? 144 : 128);
         // blocks of 16 rows, one stack each
 #pragma unroll
@@ -458,11 +459,11 @@ __global__ void __launch_bounds__(kGgThreads, 1)
             if (whole || u < 9) {
 #pragma unroll
               for (int i = 0; i < 8; i++)
-                cp_async8_g(dst + (u >> 1) * (kGgRows * 16) + (16 * q + 2 * i + lr) * 16 + (u & 1) * 8,
+                cp_async8_g(dst + (16 * q + 2 * i + lr) * 144 + u * 8,
                             src + (int64_t)wrow(g.n0, 16 * q + 2 * i + lr) * rowb + u * 8);
             }
             if (whole)
-              cp_async8_g(dst + 8 * (kGgRows * 16) + (16 * q + (lane >> 1)) * 16 + (lane & 1) * 8,
+              cp_async8_g(dst + (16 * q + (lane >> 1)) * 144 + 128 + (lane & 1) * 8,
                           src + (int64_t)wrow(g.n0, 16 * q + (lane >> 1)) * rowb + 128 + (lane & 1) * 8);
           } else {
             if (whole || u < 4) {
