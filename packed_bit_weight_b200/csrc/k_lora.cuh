@@ -2,12 +2,28 @@
 // y[i] = fp16(base[i] + s_a B_a (A_a x[i])) for the adapter a of row i, A_a
 // [rank][k] and B_a [n][rank] ("1bit.gg zyphra": the graph form base +
 // B*(A*x)).
+//
+// A few rows (decode): one launch, a thread-block cluster per row and part of
+// n (lora_token_kernel).  More rows: the rows are sorted by adapter into tiles
+// (lora_plan_kernel), the middle products A x are taken per tile with the
+// cluster's CTAs and warps sharing k (lora_shrink_kernel), and B and base are
+// streamed once per tile (lora_expand_kernel).  The bound is bytes: A and B of
+// the adapters in use, x, base and y; the products are rank / (bytes) small,
+// so legacy MMAs straight from global memory, without staging, keep up.
 #pragma once
+#include "k_gemv.cuh"
 #include "k_rows.cuh"
 
 namespace qmm {
 
 constexpr int kLoraMaxRank = 256;
+constexpr int kLoraCluster = 8;    // CTAs that share a row (or a tile)
+constexpr int kLoraThreads = 256;
+constexpr int kLoraWarps = kLoraThreads / 32;
+
+struct LoraTile {  // rows perm[start] .. perm[start + count - 1] of one adapter (a == L: no adapter)
+  int a, start, count, pad;
+};
 
 struct LoraArgs {
   const uint16_t* a;       // [L] stacks of [R][k], a_stride bytes apart
@@ -20,7 +36,13 @@ struct LoraArgs {
   const uint16_t* x;
   const uint16_t* base;    // [m][n]; may be y
   uint16_t* y;
-  float* h;                // workspace [m][R]
+  // workspace
+  int32_t* offsets;        // [L + 2]
+  int32_t* perm;           // [m]
+  LoraTile* tiles;
+  int32_t* num_tiles;
+  float* h;                // [m][R] in the order of perm
+  int T;                   // rows per tile
 };
 
 // Rank in use of adapter a (bad values are reported and clamped).
@@ -32,58 +54,456 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& p, int a) {
   return c;
 }
 
-// One warp per (row, rank index): h[i][r] = sum_k A_a[r][k] x[i][k] in fp32.
-__global__ void __launch_bounds__(256) lora_shrink_simple_kernel(const LoraArgs p) {
-  pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int64_t i = w / p.R;
-  const int r = (int)(w - i * p.R);
-  if (i >= p.m) return;
-  const int a = p.ids[i];
-  if (a < 0 || a >= p.L) {
-    if (a != -1) raise_error(ERR_BAD_EXPERT);
-    return;
-  }
-  float s = 0.f;
-  if (r < lora_rank(p, a)) {
-    const uint4* ap = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p.a) + a * p.a_stride) +
-                      (int64_t)r * (p.k / 8);
-    const uint4* xp = reinterpret_cast<const uint4*>(p.x) + i * (p.k / 8);
-    for (int j = lane; j < p.k / 8; j += 32) {
-      const uint4 u = ap[j], v = xp[j];
-      const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const float2 f = f16x2_to_f32x2(uw[q]), g = f16x2_to_f32x2(vw[q]);
-        s = fmaf(f.x, g.x, s);
-        s = fmaf(f.y, g.y, s);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  }
-  if (lane == 0) p.h[i * p.R + r] = s;
+__device__ __forceinline__ const uint16_t* lora_a(const LoraArgs& p, int a) {
+  return reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(p.a) + a * p.a_stride);
+}
+__device__ __forceinline__ const uint16_t* lora_b(const LoraArgs& p, int a) {
+  return reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(p.b) + a * p.b_stride);
 }
 
-// One thread per output.
-__global__ void __launch_bounds__(256) lora_expand_simple_kernel(const LoraArgs p) {
+__device__ __forceinline__ float dot8(const uint4& u, const uint4& v, float s) {
+  const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; q++) {
+    const float2 f = f16x2_to_f32x2(uw[q]), g = f16x2_to_f32x2(vw[q]);
+    s = fmaf(f.x, g.x, s);
+    s = fmaf(f.y, g.y, s);
+  }
+  return s;
+}
+__device__ __forceinline__ float dot8f(const uint4& u, const float (&h)[8], float s) {
+  const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int q = 0; q < 4; q++) {
+    const float2 f = f16x2_to_f32x2(uw[q]);
+    s = fmaf(f.x, h[2 * q], s);
+    s = fmaf(f.y, h[2 * q + 1], s);
+  }
+  return s;
+}
+
+// Elements of an 8-value piece that lie at or past `left` set to zero (what a
+// rank leaves out is never used, whatever it holds).
+__device__ __forceinline__ uint4 mask8(uint4 v, int left) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; q++) {
+    if (2 * q >= left) w[q] = 0u;
+    else if (2 * q + 1 >= left) w[q] &= 0xFFFFu;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------------------
+// Decode: a cluster of 8 CTAs per (row, part of n).  CTA q multiplies R/8 rows
+// of A with x (every warp an eighth of k, the partial sums joined in warp
+// order), the CTAs read each other's values through distributed shared memory,
+// and each goes on with its own rows of B: rank/8 lanes a row (rounded up to a
+// power of two), 16 bytes each, the first of them loaded before the exchange.
+// At one row all of it is latency: a launch, two dependent reads (the id, then
+// A), a cluster barrier.
+// ---------------------------------------------------------------------------
+__global__ void __cluster_dims__(kLoraCluster, 1, 1) __launch_bounds__(kLoraThreads)
+    lora_token_kernel(const LoraArgs p, int parts) {
+  __shared__ float red[kLoraWarps][kLoraMaxRank / kLoraCluster];
+  __shared__ float mine[kLoraMaxRank / kLoraCluster];
+  __shared__ float h[kLoraMaxRank];
   pdl_enter();
-  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t i = q / p.n;
-  const int c = (int)(q - i * p.n);
-  if (i >= p.m) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int q = (int)cluster_ctarank();
+  const int cl = blockIdx.x / kLoraCluster;
+  const int i = cl / parts, part = cl - i * parts;
+  const int64_t row = i;
+  // this CTA's outputs
+  const int slices = parts * kLoraCluster, slice = part * kLoraCluster + q;
+  const int per = ((p.n + slices - 1) / slices + 7) & ~7;
+  const int c0 = min(slice * per, p.n), c1 = min(c0 + per, p.n);
   const int a = p.ids[i];
-  if (a < 0 || a >= p.L) {
-    p.y[q] = p.base[q];
+  if (a < 0 || a >= p.L) {  // the whole cluster
+    if (a != -1) raise_error(ERR_BAD_EXPERT);
+    if (p.base != p.y)
+      for (int c = c0 + tid; c < c1; c += kLoraThreads) p.y[row * p.n + c] = p.base[row * p.n + c];
     return;
   }
   const int rank = lora_rank(p, a);
-  const uint16_t* bp = reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(p.b) + a * p.b_stride) +
-                       (int64_t)c * p.R;
-  float s = 0.f;
-  for (int r = 0; r < rank; r++) s = fmaf(p.h[i * p.R + r], __half2float(__ushort_as_half(bp[r])), s);
-  p.y[q] = f32_to_f16_bits(fmaf(p.scales[a], s, __half2float(__ushort_as_half(p.base[q]))));
+  const float scale = p.scales[a];
+  const int R = p.R, k8 = p.k >> 3;
+  // expand geometry: lpr lanes per row of B, 32 / lpr rows per warp and step
+  int lpr = 1;
+  while (lpr * 8 < R) lpr *= 2;
+  const int sub = lane & (lpr - 1), rows = 32 / lpr, r0 = sub * 8;
+  const uint16_t* B = lora_b(p, a);
+  constexpr int kPre = 4;  // steps loaded ahead
+  uint4 pre[kPre];
+  auto b_row = [&](int c) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (c < c1 && r0 < rank) {
+      v = *reinterpret_cast<const uint4*>(B + (int64_t)c * R + r0);
+      if (r0 + 8 > rank) v = mask8(v, rank - r0);
+    }
+    return v;
+  };
+  const int cw = c0 + warp * rows + lane / lpr;  // this lane's first row of B
+#pragma unroll
+  for (int u = 0; u < kPre; u++) pre[u] = b_row(cw + u * rows * kLoraWarps);
+
+  // ---- h rows q Rc .. q Rc + Rc - 1 ----
+  const int Rc = R / kLoraCluster;
+  const uint4* xp = reinterpret_cast<const uint4*>(p.x) + row * k8;
+  const uint4* A = reinterpret_cast<const uint4*>(lora_a(p, a));
+  for (int b = 0; b < Rc; b += 8) {
+    float acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) acc[j] = 0.f;
+#pragma unroll 2
+    for (int c = tid; c < k8; c += kLoraThreads) {
+      const uint4 xv = xp[c];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const int r = q * Rc + b + j;
+        if (b + j < Rc && r < rank) acc[j] = dot8(A[(int64_t)r * k8 + c], xv, acc[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      if (b + j >= Rc) break;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], o);
+      if (lane == 0) red[warp][b + j] = acc[j];
+    }
+  }
+  __syncthreads();
+  if (tid < Rc) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kLoraWarps; w++) s += red[w][tid];
+    mine[tid] = s;
+  }
+  __syncwarp();
+  cluster_sync();
+  if (tid < R) h[tid] = ld_dsmem_f32(&mine[tid % Rc], (uint32_t)(tid / Rc));
+  __syncwarp();
+  cluster_sync();  // (no CTA leaves while another reads its values; h is complete here too)
+
+  // ---- this CTA's rows of B ----
+  float hv[8];
+#pragma unroll
+  for (int j = 0; j < 8; j++) hv[j] = r0 + j < R ? h[min(r0 + j, kLoraMaxRank - 1)] : 0.f;
+  for (int c = cw, step = 0; c - lane / lpr < c1; step++) {
+    uint4 v[kPre];
+    if (step == 0) {
+#pragma unroll
+      for (int u = 0; u < kPre; u++) v[u] = pre[u];
+    } else {
+#pragma unroll
+      for (int u = 0; u < kPre; u++) v[u] = b_row(c + u * rows * kLoraWarps);
+    }
+#pragma unroll
+    for (int u = 0; u < kPre; u++) {
+      float s = dot8f(v[u], hv, 0.f);
+      for (int o = lpr >> 1; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      const int cc = c + u * rows * kLoraWarps;
+      if (sub == 0 && cc < c1) {
+        const int64_t at = row * p.n + cc;
+        p.y[at] = f32_to_f16_bits(fmaf(scale, s, __half2float(__ushort_as_half(p.base[at]))));
+      }
+    }
+    c += kPre * rows * kLoraWarps;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Plan: rows sorted by adapter (the stable sort of k_rows.cuh; rows without an
+// adapter come last, as adapter L) cut into tiles of at most T rows.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) lora_tiles_kernel(const LoraArgs p) {
+  pdl_enter();
+  __shared__ int warp_sum[8];
+  __shared__ int carry;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) carry = 0;
+  __syncthreads();
+  for (int e0 = 0; e0 <= p.L; e0 += 256) {
+    const int e = e0 + tid;
+    int start = 0, cnt = 0;
+    if (e <= p.L) {
+      start = p.offsets[e];
+      cnt = p.offsets[e + 1] - start;
+      if (e == p.L && p.base == p.y) cnt = 0;  // in place: nothing to copy
+    }
+    const int t = (cnt + p.T - 1) / p.T;
+    int s = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane == 31) warp_sum[warp] = s;
+    __syncthreads();
+    int at = carry + s - t;
+    for (int w = 0; w < warp; w++) at += warp_sum[w];
+    // equal tiles of whole 16-row steps
+    const int per = t ? (((cnt + t - 1) / t) + 15) & ~15 : 0;
+    for (int j = 0; j < t; j++) {
+      LoraTile tile;
+      tile.a = e;
+      tile.start = start + j * per;
+      tile.count = max(0, min(per, cnt - j * per));
+      tile.pad = 0;
+      p.tiles[at + j] = tile;
+    }
+    __syncthreads();
+    if (tid == 255) carry = at + t;
+    __syncthreads();
+  }
+  if (tid == 0) *p.num_tiles = carry;
+}
+
+// ---------------------------------------------------------------------------
+// Middle products of a tile: h[row][r] = sum_k A[r][k] x[row][k], fp32.  The 8
+// CTAs of a cluster each take an eighth of k (in whole 32-wide chunks), and in
+// a CTA the 8 warps are mw groups of 16 rows times 8/mw shares of that.  MMA
+// m16n8k16 with the rows as M and 64 of the ranks as N; the k order inside a
+// chunk is chosen so that a lane's 16 bytes of a row are its fragment words.
+// Partial sums meet in shared memory, then across the cluster, each in a fixed
+// order.
+// ---------------------------------------------------------------------------
+__global__ void __cluster_dims__(kLoraCluster, 1, 1) __launch_bounds__(kLoraThreads)
+    lora_shrink_kernel(const LoraArgs p) {
+  extern __shared__ __align__(16) float sh[];  // [8 warps: kw][mw * 16][64] partial sums, then [T][64] of this CTA
+  __shared__ int64_t xrow[128];
+  pdl_enter();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grp = lane >> 2, tig = lane & 3;
+  const int q = (int)cluster_ctarank(), t = blockIdx.x / kLoraCluster;
+  if (t >= *p.num_tiles) return;  // the whole cluster
+  const LoraTile tile = p.tiles[t];
+  if (tile.a >= p.L || tile.count <= 0) return;
+  const int rank = lora_rank(p, tile.a), R = p.R;
+  for (int i = tid; i < tile.count; i += kLoraThreads) xrow[i] = (int64_t)p.perm[tile.start + i] * p.k;
+  __syncthreads();
+  int mw = 1;
+  while (mw * 16 < tile.count) mw *= 2;
+  const int kw = kLoraWarps / mw;
+  const int mg = warp % mw, ks = warp / mw;
+  const int chunks = (p.k + 31) >> 5, shares = kLoraCluster * kw, share = q * kw + ks;
+  const int ch0 = (int)((int64_t)chunks * share / shares), ch1 = (int)((int64_t)chunks * (share + 1) / shares);
+  const int row0 = mg * 16 + grp, row1 = row0 + 8;
+  const uint16_t* x0 = p.x + (row0 < tile.count ? xrow[row0] : xrow[0]);
+  const uint16_t* x1 = p.x + (row1 < tile.count ? xrow[row1] : xrow[0]);
+  const uint16_t* A = lora_a(p, tile.a);
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int rb = 0; rb < R; rb += 64) {
+    const int nt = min(8, (R - rb) >> 3);
+    float acc[8][4];
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+#pragma unroll
+      for (int c = 0; c < 4; c++) acc[j][c] = 0.f;
+#pragma unroll 2
+    for (int ch = ch0; ch < ch1; ch++) {
+      const int kk = ch * 32 + tig * 8;
+      const bool in = kk < p.k;  // (k % 8 == 0: a piece is inside or outside)
+      const uint4 u0 = in ? *reinterpret_cast<const uint4*>(x0 + kk) : zero;
+      const uint4 u1 = in ? *reinterpret_cast<const uint4*>(x1 + kk) : zero;
+      uint4 w[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++)
+        w[j] = (in && j < nt && rb + 8 * j + grp < rank)
+                   ? *reinterpret_cast<const uint4*>(A + (int64_t)(rb + 8 * j + grp) * p.k + kk)
+                   : zero;
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        if (j >= nt) break;
+        mma_16816(acc[j], u0.x, u1.x, u0.y, u1.y, w[j].x, w[j].y);
+        mma_16816(acc[j], u0.z, u1.z, u0.w, u1.w, w[j].z, w[j].w);
+      }
+    }
+    // partial sums [ks][row][64]
+    float* mine = sh + (int64_t)(ks * mw * 16) * 64;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const int c = 8 * j + 2 * tig;
+      *reinterpret_cast<float2*>(mine + row0 * 64 + c) = make_float2(acc[j][0], acc[j][1]);
+      *reinterpret_cast<float2*>(mine + row1 * 64 + c) = make_float2(acc[j][2], acc[j][3]);
+    }
+    __syncthreads();
+    const int cells = mw * 16 * 64;
+    if (kw > 1)
+      for (int i = tid; i < cells; i += kLoraThreads) {
+        float s = sh[i];
+        for (int j = 1; j < kw; j++) s += sh[j * cells + i];
+        sh[i] = s;
+      }
+    __syncwarp();
+    cluster_sync();
+    // this CTA joins an eighth of the tile's cells
+    const int width = min(64, R - rb);
+    for (int i = q * kLoraThreads + tid; i < tile.count * 64; i += kLoraCluster * kLoraThreads) {
+      const int r = i & 63;
+      if (r >= width) continue;
+      float s = 0.f;
+#pragma unroll
+      for (int c = 0; c < kLoraCluster; c++) s += ld_dsmem_f32(sh + i, (uint32_t)c);
+      p.h[(int64_t)(tile.start + (i >> 6)) * R + rb + r] = s;
+    }
+    __syncwarp();
+    cluster_sync();  // the partial sums are read: the next block of ranks, or the end
+  }
+}
+
+// ---------------------------------------------------------------------------
+// y = base + s B h for a tile's rows and a range of columns.  MMA m16n8k16
+// with the rows as M and 8 columns of y (rows of B) as N.  B goes from global
+// memory into fragments (a lane's 16 bytes of a row of B, as above) and stays
+// there for all of the tile's rows; a warp's four n-tiles are interleaved so
+// that a lane's columns are 8 neighbours, one 16-byte piece of base and y.
+//
+// The middle product is held as two fp16 halves, h = 2^e (hi + lo): each row
+// is scaled by a power of two that brings its largest finite value to
+// [2^14, 2^15), hi is the rounded value and lo the rounded rest, so h keeps 22
+// bits (off by 2^-22 where one fp16 would be off by 2^-12) at twice the MMAs,
+// which the stream of base and y hides.
+// ---------------------------------------------------------------------------
+template <int KC>  // 32-wide chunks of the rank: R <= 32 KC
+__global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArgs p) {
+  extern __shared__ __align__(16) uint4 frag[];  // [row group][chunk][step][hi, lo][lane] fragments of h
+  __shared__ int yrow[128];
+  __shared__ float pow2[128];
+  pdl_enter();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grp = lane >> 2, tig = lane & 3;
+  if ((int)blockIdx.y >= *p.num_tiles) return;
+  const LoraTile tile = p.tiles[blockIdx.y];
+  if (tile.count <= 0) return;
+  const int n = p.n, R = p.R;
+  const int per = ((n + gridDim.x * 32 - 1) / (gridDim.x * 32)) * 32;
+  const int c0 = blockIdx.x * per, c1 = min(c0 + per, n);
+  if (c0 >= c1) return;
+  for (int i = tid; i < tile.count; i += kLoraThreads) yrow[i] = p.perm[tile.start + i];
+  __syncthreads();
+  if (tile.a >= p.L) {  // rows without an adapter
+    for (int i = warp; i < tile.count; i += kLoraWarps) {
+      const int64_t at = (int64_t)yrow[i] * n;
+      for (int c = c0 + lane; c < c1; c += 32) p.y[at + c] = p.base[at + c];
+    }
+    return;
+  }
+  const int rank = lora_rank(p, tile.a);
+  const float scale = p.scales[tile.a];
+  const int groups = (tile.count + 15) >> 4;
+  // fragments of h: a warp per row
+  for (int i = warp; i < groups * 16; i += kLoraWarps) {
+    const float* hr = p.h + (int64_t)(tile.start + i) * R;
+    float v[KC];
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < KC; c++) {
+      v[c] = (i < tile.count && 32 * c + lane < R) ? hr[32 * c + lane] : 0.f;
+      const float f = fabsf(v[c]);
+      if (f <= 3.4028235e38f) top = fmaxf(top, f);  // (finite)
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    // top in [2^e, 2^(e+1)): scaled by 2^(14 - e), in two factors so that neither leaves fp32
+    const int e = (int)(__float_as_uint(top) >> 23) - 127;
+    const int sh = top > 0.f ? min(14 - e, 126) : 0;
+    const float f1 = __uint_as_float((uint32_t)(127 + (sh >> 1)) << 23);
+    const float f2 = __uint_as_float((uint32_t)(127 + (sh - (sh >> 1))) << 23);
+    if (lane == 0) pow2[i] = __uint_as_float((uint32_t)(127 - sh) << 23);
+    // column r = 32 c + 8 t + 4 s + 2 w + b of row i: word (row half) + 2 w of lane (i % 8, t), step s of chunk c, half b
+    const int t = lane >> 3, s = (lane >> 2) & 1, w = (lane >> 1) & 1, b = lane & 1;
+    const int word = ((i >> 3) & 1) + 2 * w, to = ((i & 7) << 2) | t;
+#pragma unroll
+    for (int c = 0; c < KC; c++) {
+      const float x = v[c] * f1 * f2;
+      const __half hi = __float2half_rn(x);
+      const float back = __half2float(hi);
+      const bool finite = fabsf(back) <= 65504.f;
+      const __half lo = finite ? __float2half_rn(x - back) : __float2half_rn(0.f);
+      __half* f = reinterpret_cast<__half*>(frag + ((((i >> 4) * KC + c) * 2 + s) * 2) * 32 + to);
+      f[word * 2 + b] = hi;
+      f[32 * 8 + word * 2 + b] = lo;
+    }
+  }
+  __syncthreads();
+  const uint16_t* B = lora_b(p, tile.a);
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const bool vec = (n & 7) == 0;
+  for (int nb = c0 + warp * 32; nb < c1; nb += kLoraWarps * 32) {
+    uint4 w[4][KC];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const int col = nb + 8 * (grp >> 1) + 2 * j + (grp & 1);
+#pragma unroll
+      for (int c = 0; c < KC; c++) {
+        const int r = 32 * c + 8 * tig;
+        w[j][c] = zero;
+        if (col < n && r < rank) {
+          w[j][c] = *reinterpret_cast<const uint4*>(B + (int64_t)col * R + r);
+          if (r + 8 > rank) w[j][c] = mask8(w[j][c], rank - r);
+        }
+      }
+    }
+    const int col = nb + 8 * tig;  // this lane's 8 columns
+    for (int g = 0; g < groups; g++) {
+      const int i0 = g * 16 + grp, i1 = i0 + 8;
+      const bool ok0 = i0 < tile.count, ok1 = i1 < tile.count;
+      const int64_t at0 = (int64_t)yrow[ok0 ? i0 : 0] * n + col, at1 = (int64_t)yrow[ok1 ? i1 : 0] * n + col;
+      uint4 b0 = zero, b1 = zero;
+      if (vec) {
+        if (ok0 && col < c1) b0 = *reinterpret_cast<const uint4*>(p.base + at0);
+        if (ok1 && col < c1) b1 = *reinterpret_cast<const uint4*>(p.base + at1);
+      }
+      float acc[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+#pragma unroll
+        for (int c = 0; c < 4; c++) acc[j][c] = 0.f;
+#pragma unroll
+      for (int c = 0; c < KC; c++) {
+        if (32 * c >= rank) break;
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+          const uint4* f = frag + (((g * KC + c) * 2 + s) * 2) * 32 + lane;
+          const uint4 hi = f[0], lo = f[32];
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const uint32_t v0 = s ? w[j][c].z : w[j][c].x, v1 = s ? w[j][c].w : w[j][c].y;
+            mma_16816(acc[j], hi.x, hi.y, hi.z, hi.w, v0, v1);
+            mma_16816(acc[j], lo.x, lo.y, lo.z, lo.w, v0, v1);
+          }
+        }
+      }
+      // acc[j][0..1]: row i0, columns col + 2j, + 1; acc[j][2..3]: row i1
+      const float q0 = pow2[i0], q1 = pow2[i1];
+      if (vec) {
+        const uint32_t bw0[4] = {b0.x, b0.y, b0.z, b0.w}, bw1[4] = {b1.x, b1.y, b1.z, b1.w};
+        uint32_t o0[4], o1[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const float2 f0 = f16x2_to_f32x2(bw0[j]), f1 = f16x2_to_f32x2(bw1[j]);
+          o0[j] = f32x2_to_f16x2(fmaf(scale, acc[j][0] * q0, f0.x), fmaf(scale, acc[j][1] * q0, f0.y));
+          o1[j] = f32x2_to_f16x2(fmaf(scale, acc[j][2] * q1, f1.x), fmaf(scale, acc[j][3] * q1, f1.y));
+        }
+        if (ok0 && col < c1) *reinterpret_cast<uint4*>(p.y + at0) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+        if (ok1 && col < c1) *reinterpret_cast<uint4*>(p.y + at1) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+          for (int b = 0; b < 2; b++) {
+            if (col + 2 * j + b >= c1) continue;
+            if (ok0) {
+              const int64_t at = at0 + 2 * j + b;
+              p.y[at] = f32_to_f16_bits(fmaf(scale, acc[j][b] * q0, __half2float(__ushort_as_half(p.base[at]))));
+            }
+            if (ok1) {
+              const int64_t at = at1 + 2 * j + b;
+              p.y[at] = f32_to_f16_bits(fmaf(scale, acc[j][b + 2] * q1, __half2float(__ushort_as_half(p.base[at]))));
+            }
+          }
+      }
+    }
+  }
 }
 
 }  // namespace qmm

@@ -11,7 +11,7 @@
 
 namespace qmm {
 
-constexpr int kRowsMaxBins = 1024;   // experts (or adapters) of one sort
+constexpr int kRowsMaxBins = 1024;   // experts (or adapters) of one sort, one more for rows without
 constexpr int kRowsSortWarps = 16;   // warps per CTA of the sort
 constexpr int kRowsSortThreads = kRowsSortWarps * 32;
 
@@ -44,11 +44,12 @@ __device__ __forceinline__ int ld_dsmem_s32(const int* local, uint32_t r) {
 // distributed shared memory, and a second walk over the same run writes each
 // pair's place.  ids outside [0, E) take no place; -1 says so on purpose
 // (padding, a request without an adapter), anything else raises the error.
+// With `rest` they are kept instead, as the last bin E - 1.
 // ---------------------------------------------------------------------------
 __host__ __device__ constexpr int route_rows_smem(int E) { return (kRowsSortWarps + 3) * E * 4; }
 
 __global__ void __launch_bounds__(kRowsSortThreads, 1)
-    route_rows_kernel(const int32_t* __restrict__ ids, int P, int E, int32_t* __restrict__ offsets,
+    route_rows_kernel(const int32_t* __restrict__ ids, int P, int E, int rest, int32_t* __restrict__ offsets,
                       int32_t* __restrict__ perm, int32_t* __restrict__ row_of) {
   extern __shared__ int smem_rows[];
   int* cnt = smem_rows;                      // [warp][E]: counts, then the warp's next place within its expert
@@ -67,9 +68,10 @@ __global__ void __launch_bounds__(kRowsSortThreads, 1)
   bool bad = false;
   for (int i = 0; i < steps; i++) {
     const int64_t p = p0 + i * 32 + lane;
-    const int e = p < P ? ids[p] : -1;
-    const bool valid = e >= 0 && e < E;
+    int e = p < P ? ids[p] : -1;
+    bool valid = e >= 0 && e < E - rest;
     bad |= !valid && e != -1;
+    if (rest && !valid && p < P) { e = E - 1; valid = true; }
     const unsigned peers = __match_any_sync(0xFFFFFFFFu, valid ? e : -1);
     if (valid && (peers & lt) == 0) mine[e] += __popc(peers);
     __syncwarp();
@@ -119,8 +121,9 @@ __global__ void __launch_bounds__(kRowsSortThreads, 1)
   __syncthreads();
   for (int i = 0; i < steps; i++) {
     const int64_t p = p0 + i * 32 + lane;
-    const int e = p < P ? ids[p] : -1;
-    const bool valid = e >= 0 && e < E;
+    int e = p < P ? ids[p] : -1;
+    bool valid = e >= 0 && e < E - rest;
+    if (rest && !valid && p < P) { e = E - 1; valid = true; }
     const unsigned peers = __match_any_sync(0xFFFFFFFFu, valid ? e : -1);
     int place = -1;
     if (valid) place = grand[e] + before[e] + mine[e] + __popc(peers & lt);

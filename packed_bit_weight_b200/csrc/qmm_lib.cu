@@ -1357,11 +1357,11 @@ static int sort_ctas(int64_t P) {
   return c;
 }
 
-static qmm_status launch_route_rows(const int32_t* ids, int64_t P, int64_t E, int32_t* offsets, int32_t* perm,
-                                    int32_t* row_of, cudaStream_t st) {
+static qmm_status launch_route_rows(const int32_t* ids, int64_t P, int64_t E, int rest, int32_t* offsets,
+                                    int32_t* perm, int32_t* row_of, cudaStream_t st) {
   const int smem = route_rows_smem((int)E);
   if (smem > 48 * 1024 && cudaFuncSetAttribute(route_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               route_rows_smem(kRowsMaxBins)) != cudaSuccess)
+                                               route_rows_smem(kRowsMaxBins + 1)) != cudaSuccess)
     return QMM_ERR_CUDA;
   const int cs = sort_ctas(P);
   cudaLaunchConfig_t cfg = {};
@@ -1376,7 +1376,7 @@ static qmm_status launch_route_rows(const int32_t* ids, int64_t P, int64_t E, in
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, route_rows_kernel, ids, (int)P, (int)E, offsets, perm, row_of) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, route_rows_kernel, ids, (int)P, (int)E, rest, offsets, perm, row_of) != cudaSuccess)
     return QMM_ERR_CUDA;
   return launch_status();
 }
@@ -1393,7 +1393,7 @@ qmm_status qmm_route_rows(const int32_t* topk_ids, int64_t t, int64_t topk, int6
   DevInfo* di = nullptr;
   qmm_status s = device_info(&di);
   if (s != QMM_OK) return s;
-  s = launch_route_rows(topk_ids, P, num_experts, expert_offsets, pair_perm, pair_row,
+  s = launch_route_rows(topk_ids, P, num_experts, 0, expert_offsets, pair_perm, pair_row,
                         static_cast<cudaStream_t>(stream));
   if (s == QMM_OK) set_variant("route_rows<cluster=%d>", sort_ctas(P));
   return s;
@@ -1587,9 +1587,33 @@ static qmm_status check_adapters(const qmm_adapters* ad) {
   return QMM_OK;
 }
 
+// Up to this many rows a cluster per row (lora_token_kernel): no sort, one
+// launch; above it the tiled path.
+constexpr int64_t kLoraTokenRows = 16;
+
+// Rows per tile: B and A are read once per tile, so long inputs take large
+// ones; short ones small ones, for the number of CTAs.
+static int lora_tile_rows(int64_t m) { return m >= 1024 ? 128 : m >= 512 ? 64 : 32; }
+static int64_t lora_max_tiles(int64_t L, int64_t m) { return m / lora_tile_rows(m) + std::min(m, L + 1); }
+
+// Workspace of the tiled path: offsets, permutation, tile count, tiles, h.
+struct LoraWorkspace {
+  size_t offsets, perm, num, tiles, h, bytes;
+};
+static LoraWorkspace lora_workspace(const qmm_adapters* ad, int64_t m) {
+  LoraWorkspace w = {};
+  if (m <= kLoraTokenRows || ad->rank == 0 || ad->k == 0) return w;
+  w.perm = align256(4 * (size_t)(ad->num_adapters + 2));
+  w.num = w.perm + align256(4 * (size_t)m);
+  w.tiles = w.num + 256;
+  w.h = w.tiles + align256(sizeof(LoraTile) * (size_t)lora_max_tiles(ad->num_adapters, m));
+  w.bytes = w.h + align256(4 * (size_t)m * (size_t)ad->rank);
+  return w;
+}
+
 size_t qmm_lora_workspace_bytes(const qmm_adapters* ad, int64_t m) {
   if (check_adapters(ad) != QMM_OK || m < 0 || m > INT32_MAX / 2) return 0;
-  return align256(4 * (size_t)m * (size_t)ad->rank);
+  return lora_workspace(ad, m).bytes;
 }
 
 qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* adapter_ids, int64_t m,
@@ -1604,8 +1628,16 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
     if (p && !aligned16(p)) return QMM_ERR_MISALIGNED;
   if ((s = device_info(&di)) != QMM_OK) return s;
   if (m == 0 || ad->n == 0) return QMM_OK;
-  if (ws_bytes < qmm_lora_workspace_bytes(ad, m) || (!ws && ws_bytes)) return QMM_ERR_WORKSPACE;
-  LoraArgs a;
+  const LoraWorkspace w = lora_workspace(ad, m);
+  if (w.bytes && (!ws || ws_bytes < w.bytes)) return QMM_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (ad->rank == 0 || ad->k == 0) {  // empty sums
+    if (base != y && cudaMemcpyAsync(y, base, 2 * (size_t)m * (size_t)ad->n, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
+      return QMM_ERR_CUDA;
+    set_variant("lora_copy");
+    return QMM_OK;
+  }
+  LoraArgs a = {};
   a.a = static_cast<const uint16_t*>(ad->a);
   a.b = static_cast<const uint16_t*>(ad->b);
   a.scales = ad->scales;
@@ -1621,15 +1653,46 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
   a.x = x;
   a.base = base;
   a.y = y;
-  a.h = static_cast<float*>(ws);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t b1 = (m * ad->rank + 7) / 8, b2 = (m * ad->n + 255) / 256;
-  if (b1 > INT32_MAX || b2 > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
-  if (b1 && launch_pdl(lora_shrink_simple_kernel, dim3((unsigned)b1), dim3(256), 0, st, a) != cudaSuccess)
+  if (m <= kLoraTokenRows) {
+    // parts of n per row: a CTA per SM and no fewer than 64 outputs each
+    int64_t parts = std::max<int64_t>(1, di->sms / (kLoraCluster * m));
+    parts = std::min(parts, std::max<int64_t>(1, ad->n / (64 * kLoraCluster)));
+    if (launch_pdl(lora_token_kernel, dim3((unsigned)(m * parts * kLoraCluster)), dim3(kLoraThreads), 0, st, a,
+                   (int)parts) != cudaSuccess)
+      return QMM_ERR_CUDA;
+    set_variant("lora_token<parts=%d>", (int)parts);
+    return launch_status();
+  }
+  char* base_ws = static_cast<char*>(ws);
+  a.offsets = reinterpret_cast<int32_t*>(base_ws + w.offsets);
+  a.perm = reinterpret_cast<int32_t*>(base_ws + w.perm);
+  a.num_tiles = reinterpret_cast<int32_t*>(base_ws + w.num);
+  a.tiles = reinterpret_cast<LoraTile*>(base_ws + w.tiles);
+  a.h = reinterpret_cast<float*>(base_ws + w.h);
+  a.T = lora_tile_rows(m);
+  const int64_t tiles = lora_max_tiles(ad->num_adapters, m);
+  if (tiles > 65535 || tiles * kLoraCluster > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
+  if ((s = launch_route_rows(adapter_ids, m, ad->num_adapters + 1, 1, a.offsets, a.perm, nullptr, st)) != QMM_OK)
+    return s;
+  if (launch_pdl(lora_tiles_kernel, dim3(1), dim3(256), 0, st, a) != cudaSuccess) return QMM_ERR_CUDA;
+  const int shrink_smem = 128 * 64 * 4;  // 8 warps of 16 rows x 64 sums
+  if (cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shrink_smem) != cudaSuccess)
     return QMM_ERR_CUDA;
-  if (launch_pdl(lora_expand_simple_kernel, dim3((unsigned)b2), dim3(256), 0, st, a) != cudaSuccess)
+  if (launch_pdl(lora_shrink_kernel, dim3((unsigned)(tiles * kLoraCluster)), dim3(kLoraThreads), shrink_smem, st, a) !=
+      cudaSuccess)
     return QMM_ERR_CUDA;
-  set_variant("lora_simple");
+  // columns: two CTAs an SM over the tiles that are likely there, whole 256-column steps
+  const int64_t likely = std::max<int64_t>(1, std::min(tiles, (m + a.T - 1) / a.T + std::min<int64_t>(m / 16, ad->num_adapters)));
+  int64_t cols = std::max<int64_t>(1, 2 * di->sms / likely);
+  cols = std::min(cols, (ad->n + 255) / 256);
+  const int kc = (int)((ad->rank + 31) / 32), KC = kc <= 1 ? 1 : kc <= 2 ? 2 : kc <= 4 ? 4 : 8;
+  const int smem = (a.T / 16) * KC * 4 * 32 * 16;
+  auto kern = KC == 1 ? lora_expand_kernel<1> : KC == 2 ? lora_expand_kernel<2> : KC == 4 ? lora_expand_kernel<4>
+                                                                                         : lora_expand_kernel<8>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return QMM_ERR_CUDA;
+  if (launch_pdl(kern, dim3((unsigned)cols, (unsigned)tiles), dim3(kLoraThreads), (size_t)smem, st, a) != cudaSuccess)
+    return QMM_ERR_CUDA;
+  set_variant("lora_tiled<rows=%d,chunks=%d,cols=%d>", a.T, KC, (int)cols);
   return launch_status();
 }
 
