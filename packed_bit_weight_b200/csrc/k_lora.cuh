@@ -5,7 +5,7 @@
 //
 // A few rows (decode): one launch, a thread-block cluster per row and part of
 // n (lora_token_kernel).  More rows: the rows are sorted by adapter into tiles
-// (lora_plan_kernel), the middle products A x are taken per tile with the
+// (the sort of k_rows.cuh), the middle products A x are taken per tile with the
 // cluster's CTAs and warps sharing k (lora_shrink_kernel), and B and base are
 // streamed once per tile (lora_expand_kernel).  The bound is bytes: A and B of
 // the adapters in use, x, base and y; the products are rank / (bytes) small,
@@ -21,10 +21,6 @@ constexpr int kLoraCluster = 8;    // CTAs that share a row (or a tile)
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
 
-struct LoraTile {  // rows perm[start] .. perm[start + count - 1] of one adapter (a == L: no adapter)
-  int a, start, count, pad;
-};
-
 struct LoraArgs {
   const uint16_t* a;       // [L] stacks of [R][k], a_stride bytes apart
   const uint16_t* b;       // [L] stacks of [n][R], b_stride bytes apart
@@ -39,10 +35,9 @@ struct LoraArgs {
   // workspace
   int32_t* offsets;        // [L + 2]
   int32_t* perm;           // [m]
-  LoraTile* tiles;
+  RowTile* tiles;          // g: the adapter, L for rows without one
   int32_t* num_tiles;
   float* h;                // [m][R] in the order of perm
-  int T;                   // rows per tile
 };
 
 // Rank in use of adapter a (bad values are reported and clamped).
@@ -94,6 +89,21 @@ __device__ __forceinline__ uint4 mask8(uint4 v, int left) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// y[c0 .. c1) = base[c0 .. c1) (not overlapping) by `threads` threads; vec:
+// both are 16-byte aligned at multiples of 8 columns, and c0 is one.
+__device__ __forceinline__ void copy_span(uint16_t* __restrict__ y, const uint16_t* __restrict__ base, int c0, int c1,
+                                          bool vec, int t, int threads) {
+  int c = c0;
+  if (vec) {
+#pragma unroll 4
+    for (int i = c0 + 8 * t; i + 8 <= c1; i += 8 * threads)
+      *reinterpret_cast<uint4*>(y + i) = *reinterpret_cast<const uint4*>(base + i);
+    c = c0 + ((c1 - c0) & ~7);
+  }
+#pragma unroll 4
+  for (int i = c + t; i < c1; i += threads) y[i] = base[i];
+}
+
 // ---------------------------------------------------------------------------
 // Decode: a cluster of 8 CTAs per (row, part of n).  CTA q multiplies R/8 rows
 // of A with x (every warp an eighth of k, the partial sums joined in warp
@@ -122,7 +132,7 @@ __global__ void __cluster_dims__(kLoraCluster, 1, 1) __launch_bounds__(kLoraThre
   if (a < 0 || a >= p.L) {  // the whole cluster
     if (a != -1) raise_error(ERR_BAD_EXPERT);
     if (p.base != p.y)
-      for (int c = c0 + tid; c < c1; c += kLoraThreads) p.y[row * p.n + c] = p.base[row * p.n + c];
+      copy_span(p.y + row * p.n, p.base + row * p.n, c0, c1, (p.n & 7) == 0, tid, kLoraThreads);
     return;
   }
   const int rank = lora_rank(p, a);
@@ -135,17 +145,18 @@ __global__ void __cluster_dims__(kLoraCluster, 1, 1) __launch_bounds__(kLoraThre
   const uint16_t* B = lora_b(p, a);
   constexpr int kPre = 4;  // steps loaded ahead
   uint4 pre[kPre];
+  uint16_t pre_base[kPre];
   auto b_row = [&](int c) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (c < c1 && r0 < rank) {
-      v = *reinterpret_cast<const uint4*>(B + (int64_t)c * R + r0);
-      if (r0 + 8 > rank) v = mask8(v, rank - r0);
-    }
-    return v;
+    return (c < c1 && r0 < rank) ? *reinterpret_cast<const uint4*>(B + (int64_t)c * R + r0)
+                                 : make_uint4(0u, 0u, 0u, 0u);
   };
   const int cw = c0 + warp * rows + lane / lpr;  // this lane's first row of B
 #pragma unroll
-  for (int u = 0; u < kPre; u++) pre[u] = b_row(cw + u * rows * kLoraWarps);
+  for (int u = 0; u < kPre; u++) {
+    const int c = cw + u * rows * kLoraWarps;
+    pre[u] = b_row(c);
+    pre_base[u] = c < c1 ? p.base[row * p.n + c] : (uint16_t)0;
+  }
 
   // ---- h rows q Rc .. q Rc + Rc - 1 ----
   const int Rc = R / kLoraCluster;
@@ -189,166 +200,124 @@ __global__ void __cluster_dims__(kLoraCluster, 1, 1) __launch_bounds__(kLoraThre
   float hv[8];
 #pragma unroll
   for (int j = 0; j < 8; j++) hv[j] = r0 + j < R ? h[min(r0 + j, kLoraMaxRank - 1)] : 0.f;
-  for (int c = cw, step = 0; c - lane / lpr < c1; step++) {
-    uint4 v[kPre];
-    if (step == 0) {
-#pragma unroll
-      for (int u = 0; u < kPre; u++) v[u] = pre[u];
-    } else {
-#pragma unroll
-      for (int u = 0; u < kPre; u++) v[u] = b_row(c + u * rows * kLoraWarps);
-    }
+  for (int c = cw; c - lane / lpr < c1;) {
+    // the next step's pieces are loaded before this one's outputs are stored
+    // (y may be base, so no load moves up past a store by itself)
+    uint4 next[kPre];
+    uint16_t next_base[kPre];
+    const int cn = c + kPre * rows * kLoraWarps;
 #pragma unroll
     for (int u = 0; u < kPre; u++) {
-      float s = dot8f(v[u], hv, 0.f);
-      for (int o = lpr >> 1; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      const int cc = cn + u * rows * kLoraWarps;
+      next[u] = b_row(cc);
+      next_base[u] = cc < c1 ? p.base[row * p.n + cc] : (uint16_t)0;
+    }
+    float s[kPre];
+#pragma unroll
+    for (int u = 0; u < kPre; u++) s[u] = dot8f((rank & 7) ? mask8(pre[u], rank - r0) : pre[u], hv, 0.f);
+    for (int o = lpr >> 1; o; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < kPre; u++) s[u] += __shfl_xor_sync(0xFFFFFFFFu, s[u], o);
+#pragma unroll
+    for (int u = 0; u < kPre; u++) {
       const int cc = c + u * rows * kLoraWarps;
-      if (sub == 0 && cc < c1) {
-        const int64_t at = row * p.n + cc;
-        p.y[at] = f32_to_f16_bits(fmaf(scale, s, __half2float(__ushort_as_half(p.base[at]))));
-      }
+      if (sub == 0 && cc < c1)
+        p.y[row * p.n + cc] = f32_to_f16_bits(fmaf(scale, s[u], __half2float(__ushort_as_half(pre_base[u]))));
+      pre[u] = next[u];
+      pre_base[u] = next_base[u];
     }
     c += kPre * rows * kLoraWarps;
   }
 }
 
 // ---------------------------------------------------------------------------
-// Plan: rows sorted by adapter (the stable sort of k_rows.cuh; rows without an
-// adapter come last, as adapter L) cut into tiles of at most T rows.
-// ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) lora_tiles_kernel(const LoraArgs p) {
-  pdl_enter();
-  __shared__ int warp_sum[8];
-  __shared__ int carry;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) carry = 0;
-  __syncthreads();
-  for (int e0 = 0; e0 <= p.L; e0 += 256) {
-    const int e = e0 + tid;
-    int start = 0, cnt = 0;
-    if (e <= p.L) {
-      start = p.offsets[e];
-      cnt = p.offsets[e + 1] - start;
-      if (e == p.L && p.base == p.y) cnt = 0;  // in place: nothing to copy
-    }
-    const int t = (cnt + p.T - 1) / p.T;
-    int s = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-      if (lane >= o) s += u;
-    }
-    if (lane == 31) warp_sum[warp] = s;
-    __syncthreads();
-    int at = carry + s - t;
-    for (int w = 0; w < warp; w++) at += warp_sum[w];
-    // equal tiles of whole 16-row steps
-    const int per = t ? (((cnt + t - 1) / t) + 15) & ~15 : 0;
-    for (int j = 0; j < t; j++) {
-      LoraTile tile;
-      tile.a = e;
-      tile.start = start + j * per;
-      tile.count = max(0, min(per, cnt - j * per));
-      tile.pad = 0;
-      p.tiles[at + j] = tile;
-    }
-    __syncthreads();
-    if (tid == 255) carry = at + t;
-    __syncthreads();
-  }
-  if (tid == 0) *p.num_tiles = carry;
-}
-
-// ---------------------------------------------------------------------------
-// Middle products of a tile: h[row][r] = sum_k A[r][k] x[row][k], fp32.  The 8
-// CTAs of a cluster each take an eighth of k (in whole 32-wide chunks), and in
+// Middle products of a tile: h[row][r] = sum_k A[r][k] x[row][k], fp32.  The
+// CTAs of a cluster each take a share of k (in whole 32-wide chunks), and in
 // a CTA the 8 warps are mw groups of 16 rows times 8/mw shares of that.  MMA
 // m16n8k16 with the rows as M and 64 of the ranks as N; the k order inside a
 // chunk is chosen so that a lane's 16 bytes of a row are its fragment words.
 // Partial sums meet in shared memory, then across the cluster, each in a fixed
 // order.
 // ---------------------------------------------------------------------------
-__global__ void __cluster_dims__(kLoraCluster, 1, 1) __launch_bounds__(kLoraThreads)
-    lora_shrink_kernel(const LoraArgs p) {
-  extern __shared__ __align__(16) float sh[];  // [8 warps: kw][mw * 16][64] partial sums, then [T][64] of this CTA
+__global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const LoraArgs p) {
+  extern __shared__ __align__(16) float sh[];  // [kw][mw * 16][64] partial sums, then [mw * 16][64] of this CTA
   __shared__ int64_t xrow[128];
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grp = lane >> 2, tig = lane & 3;
-  const int q = (int)cluster_ctarank(), t = blockIdx.x / kLoraCluster;
+  const int q = (int)cluster_ctarank(), cs = (int)cluster_nctarank(), t = blockIdx.x / cs;
   if (t >= *p.num_tiles) return;  // the whole cluster
-  const LoraTile tile = p.tiles[t];
-  if (tile.a >= p.L || tile.count <= 0) return;
-  const int rank = lora_rank(p, tile.a), R = p.R;
+  const RowTile tile = p.tiles[t];
+  if (tile.g >= p.L || tile.count <= 0) return;
+  const int rank = lora_rank(p, tile.g), R = p.R;
   for (int i = tid; i < tile.count; i += kLoraThreads) xrow[i] = (int64_t)p.perm[tile.start + i] * p.k;
   __syncthreads();
   int mw = 1;
   while (mw * 16 < tile.count) mw *= 2;
   const int kw = kLoraWarps / mw;
   const int mg = warp % mw, ks = warp / mw;
-  const int chunks = (p.k + 31) >> 5, shares = kLoraCluster * kw, share = q * kw + ks;
+  const int chunks = (p.k + 31) >> 5, shares = cs * kw, share = q * kw + ks;
   const int ch0 = (int)((int64_t)chunks * share / shares), ch1 = (int)((int64_t)chunks * (share + 1) / shares);
   const int row0 = mg * 16 + grp, row1 = row0 + 8;
   const uint16_t* x0 = p.x + (row0 < tile.count ? xrow[row0] : xrow[0]);
   const uint16_t* x1 = p.x + (row1 < tile.count ? xrow[row1] : xrow[0]);
-  const uint16_t* A = lora_a(p, tile.a);
+  const uint16_t* A = lora_a(p, tile.g);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  for (int rb = 0; rb < R; rb += 64) {
-    const int nt = min(8, (R - rb) >> 3);
-    float acc[8][4];
+  const int rb = blockIdx.y * 64;  // this CTA's block of ranks
+  const int nt = min(8, (R - rb) >> 3);
+  float acc[8][4];
+#pragma unroll
+  for (int j = 0; j < 8; j++)
+#pragma unroll
+    for (int c = 0; c < 4; c++) acc[j][c] = 0.f;
+#pragma unroll 2
+  for (int ch = ch0; ch < ch1; ch++) {
+    const int kk = ch * 32 + tig * 8;
+    const bool in = kk < p.k;  // (k % 8 == 0: a piece is inside or outside)
+    const uint4 u0 = in ? *reinterpret_cast<const uint4*>(x0 + kk) : zero;
+    const uint4 u1 = in ? *reinterpret_cast<const uint4*>(x1 + kk) : zero;
+    uint4 w[8];
 #pragma unroll
     for (int j = 0; j < 8; j++)
-#pragma unroll
-      for (int c = 0; c < 4; c++) acc[j][c] = 0.f;
-#pragma unroll 2
-    for (int ch = ch0; ch < ch1; ch++) {
-      const int kk = ch * 32 + tig * 8;
-      const bool in = kk < p.k;  // (k % 8 == 0: a piece is inside or outside)
-      const uint4 u0 = in ? *reinterpret_cast<const uint4*>(x0 + kk) : zero;
-      const uint4 u1 = in ? *reinterpret_cast<const uint4*>(x1 + kk) : zero;
-      uint4 w[8];
-#pragma unroll
-      for (int j = 0; j < 8; j++)
-        w[j] = (in && j < nt && rb + 8 * j + grp < rank)
-                   ? *reinterpret_cast<const uint4*>(A + (int64_t)(rb + 8 * j + grp) * p.k + kk)
-                   : zero;
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        if (j >= nt) break;
-        mma_16816(acc[j], u0.x, u1.x, u0.y, u1.y, w[j].x, w[j].y);
-        mma_16816(acc[j], u0.z, u1.z, u0.w, u1.w, w[j].z, w[j].w);
-      }
-    }
-    // partial sums [ks][row][64]
-    float* mine = sh + (int64_t)(ks * mw * 16) * 64;
+      w[j] = (in && j < nt && rb + 8 * j + grp < rank)
+                 ? *reinterpret_cast<const uint4*>(A + (int64_t)(rb + 8 * j + grp) * p.k + kk)
+                 : zero;
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      const int c = 8 * j + 2 * tig;
-      *reinterpret_cast<float2*>(mine + row0 * 64 + c) = make_float2(acc[j][0], acc[j][1]);
-      *reinterpret_cast<float2*>(mine + row1 * 64 + c) = make_float2(acc[j][2], acc[j][3]);
+      if (j >= nt) break;
+      mma_16816(acc[j], u0.x, u1.x, u0.y, u1.y, w[j].x, w[j].y);
+      mma_16816(acc[j], u0.z, u1.z, u0.w, u1.w, w[j].z, w[j].w);
     }
-    __syncthreads();
-    const int cells = mw * 16 * 64;
-    if (kw > 1)
-      for (int i = tid; i < cells; i += kLoraThreads) {
-        float s = sh[i];
-        for (int j = 1; j < kw; j++) s += sh[j * cells + i];
-        sh[i] = s;
-      }
-    __syncwarp();
-    cluster_sync();
-    // this CTA joins an eighth of the tile's cells
-    const int width = min(64, R - rb);
-    for (int i = q * kLoraThreads + tid; i < tile.count * 64; i += kLoraCluster * kLoraThreads) {
-      const int r = i & 63;
-      if (r >= width) continue;
-      float s = 0.f;
-#pragma unroll
-      for (int c = 0; c < kLoraCluster; c++) s += ld_dsmem_f32(sh + i, (uint32_t)c);
-      p.h[(int64_t)(tile.start + (i >> 6)) * R + rb + r] = s;
-    }
-    __syncwarp();
-    cluster_sync();  // the partial sums are read: the next block of ranks, or the end
   }
+  // partial sums [ks][row][64]
+  float* mine = sh + (int64_t)(ks * mw * 16) * 64;
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    const int c = 8 * j + 2 * tig;
+    *reinterpret_cast<float2*>(mine + row0 * 64 + c) = make_float2(acc[j][0], acc[j][1]);
+    *reinterpret_cast<float2*>(mine + row1 * 64 + c) = make_float2(acc[j][2], acc[j][3]);
+  }
+  __syncthreads();
+  const int cells = mw * 16 * 64;
+  if (kw > 1)
+    for (int i = tid; i < cells; i += kLoraThreads) {
+      float s = sh[i];
+      for (int j = 1; j < kw; j++) s += sh[j * cells + i];
+      sh[i] = s;
+    }
+  __syncthreads();
+  cluster_sync();
+  // this CTA joins its share of the tile's cells
+  const int width = min(64, R - rb);
+  for (int i = q * kLoraThreads + tid; i < tile.count * 64; i += cs * kLoraThreads) {
+    const int r = i & 63;
+    if (r >= width) continue;
+    float s = 0.f;
+#pragma unroll 8
+    for (int c = 0; c < cs; c++) s += ld_dsmem_f32(sh + i, (uint32_t)c);
+    p.h[(int64_t)(tile.start + (i >> 6)) * R + rb + r] = s;
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while its partial sums are read
 }
 
 // ---------------------------------------------------------------------------
@@ -365,40 +334,50 @@ __global__ void __cluster_dims__(kLoraCluster, 1, 1) __launch_bounds__(kLoraThre
 // which the stream of base and y hides.
 // ---------------------------------------------------------------------------
 template <int KC>  // 32-wide chunks of the rank: R <= 32 KC
-__global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArgs p) {
+__global__ void __launch_bounds__(kLoraThreads, KC <= 4 ? 2 : 1) lora_expand_kernel(const LoraArgs p) {
   extern __shared__ __align__(16) uint4 frag[];  // [row group][chunk][step][hi, lo][lane] fragments of h
   __shared__ int yrow[128];
   __shared__ float pow2[128];
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grp = lane >> 2, tig = lane & 3;
-  if ((int)blockIdx.y >= *p.num_tiles) return;
-  const LoraTile tile = p.tiles[blockIdx.y];
-  if (tile.count <= 0) return;
-  const int n = p.n, R = p.R;
-  const int per = ((n + gridDim.x * 32 - 1) / (gridDim.x * 32)) * 32;
-  const int c0 = blockIdx.x * per, c1 = min(c0 + per, n);
-  if (c0 >= c1) return;
+  // the tiles times as many column ranges as give every CTA of the grid one
+  // item (the number of tiles is known only here)
+  const int num = *p.num_tiles, n = p.n, R = p.R;
+  const int cols = num > 0 ? min(max((int)gridDim.x / num, 1), (n + 255) / 256) : 1;
+  const int per = ((n + cols * 32 - 1) / (cols * 32)) * 32;
+  for (int item = blockIdx.x; item < num * cols; item += gridDim.x) {
+  const RowTile tile = p.tiles[item / cols];
+  const int c0 = (item % cols) * per, c1 = min(c0 + per, n);
+  if (tile.count <= 0 || c0 >= c1) continue;
+  __syncthreads();  // (the last item's rows and fragments are no longer read)
   for (int i = tid; i < tile.count; i += kLoraThreads) yrow[i] = p.perm[tile.start + i];
-  __syncthreads();
-  if (tile.a >= p.L) {  // rows without an adapter
+  if (tile.g >= p.L) {  // rows without an adapter
+    __syncthreads();
     for (int i = warp; i < tile.count; i += kLoraWarps) {
       const int64_t at = (int64_t)yrow[i] * n;
-      for (int c = c0 + lane; c < c1; c += 32) p.y[at + c] = p.base[at + c];
+      copy_span(p.y + at, p.base + at, c0, c1, (n & 7) == 0, lane, 32);
     }
-    return;
+    continue;
   }
-  const int rank = lora_rank(p, tile.a);
-  const float scale = p.scales[tile.a];
+  const int rank = lora_rank(p, tile.g);
+  const float scale = p.scales[tile.g];
   const int groups = (tile.count + 15) >> 4;
-  // fragments of h: a warp per row
-  for (int i = warp; i < groups * 16; i += kLoraWarps) {
-    const float* hr = p.h + (int64_t)(tile.start + i) * R;
-    float v[KC];
+  // fragments of h: two rows per warp at a time
+  for (int i0 = warp * 2; i0 < groups * 16; i0 += kLoraWarps * 2) {
+    float v[2][KC];
+#pragma unroll
+    for (int r = 0; r < 2; r++)
+#pragma unroll
+      for (int c = 0; c < KC; c++)
+        v[r][c] = (i0 + r < tile.count && 32 * c + lane < R) ? p.h[(int64_t)(tile.start + i0 + r) * R + 32 * c + lane]
+                                                             : 0.f;
+#pragma unroll
+    for (int r = 0; r < 2; r++) {
+    const int i = i0 + r;
     float top = 0.f;
 #pragma unroll
     for (int c = 0; c < KC; c++) {
-      v[c] = (i < tile.count && 32 * c + lane < R) ? hr[32 * c + lane] : 0.f;
-      const float f = fabsf(v[c]);
+      const float f = fabsf(v[r][c]);
       if (f <= 3.4028235e38f) top = fmaxf(top, f);  // (finite)
     }
 #pragma unroll
@@ -414,7 +393,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
     const int word = ((i >> 3) & 1) + 2 * w, to = ((i & 7) << 2) | t;
 #pragma unroll
     for (int c = 0; c < KC; c++) {
-      const float x = v[c] * f1 * f2;
+      const float x = v[r][c] * f1 * f2;
       const __half hi = __float2half_rn(x);
       const float back = __half2float(hi);
       const bool finite = fabsf(back) <= 65504.f;
@@ -423,9 +402,10 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
       f[word * 2 + b] = hi;
       f[32 * 8 + word * 2 + b] = lo;
     }
+    }
   }
   __syncthreads();
-  const uint16_t* B = lora_b(p, tile.a);
+  const uint16_t* B = lora_b(p, tile.g);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   const bool vec = (n & 7) == 0;
   for (int nb = c0 + warp * 32; nb < c1; nb += kLoraWarps * 32) {
@@ -436,23 +416,46 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
 #pragma unroll
       for (int c = 0; c < KC; c++) {
         const int r = 32 * c + 8 * tig;
-        w[j][c] = zero;
-        if (col < n && r < rank) {
-          w[j][c] = *reinterpret_cast<const uint4*>(B + (int64_t)col * R + r);
-          if (r + 8 > rank) w[j][c] = mask8(w[j][c], rank - r);
-        }
+        w[j][c] = (col < n && r < rank) ? *reinterpret_cast<const uint4*>(B + (int64_t)col * R + r) : zero;
       }
     }
+    // the next columns' rows of B on their way into L2 meanwhile
+    const int ncol = nb + kLoraWarps * 32 + lane;
+    if (ncol < c1)
+      for (int r = 0; r < rank; r += 64)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(B + (int64_t)ncol * R + r));
     const int col = nb + 8 * tig;  // this lane's 8 columns
-    for (int g = 0; g < groups; g++) {
+    // base, kAhead row groups ahead of its use (loads stay behind the stores
+    // they follow: y may be base)
+    constexpr int kAhead = KC <= 4 ? 3 : 1;
+    uint4 ahead[kAhead][2];
+    auto load_base = [&](int g, uint4 (&v)[2]) {
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const int i = g * 16 + grp + 8 * h;
+        v[h] = (vec && i < tile.count && col < c1)
+                   ? *reinterpret_cast<const uint4*>(p.base + (int64_t)yrow[i] * n + col)
+                   : zero;
+      }
+    };
+#pragma unroll
+    for (int d = 0; d < kAhead; d++) load_base(d, ahead[d]);
+    if (rank & 7) {  // (after the loads: a use between them would make each wait for the last)
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+#pragma unroll
+        for (int c = 0; c < KC; c++) w[j][c] = mask8(w[j][c], rank - (32 * c + 8 * tig));
+    }
+    for (int g0 = 0; g0 < groups; g0 += kAhead) {
+#pragma unroll
+    for (int d = 0; d < kAhead; d++) {
+      const int g = g0 + d;
+      if (g >= groups) break;
       const int i0 = g * 16 + grp, i1 = i0 + 8;
       const bool ok0 = i0 < tile.count, ok1 = i1 < tile.count;
       const int64_t at0 = (int64_t)yrow[ok0 ? i0 : 0] * n + col, at1 = (int64_t)yrow[ok1 ? i1 : 0] * n + col;
-      uint4 b0 = zero, b1 = zero;
-      if (vec) {
-        if (ok0 && col < c1) b0 = *reinterpret_cast<const uint4*>(p.base + at0);
-        if (ok1 && col < c1) b1 = *reinterpret_cast<const uint4*>(p.base + at1);
-      }
+      const uint4 b0 = ahead[d][0], b1 = ahead[d][1];
+      load_base(g + kAhead, ahead[d]);
       float acc[4][4];
 #pragma unroll
       for (int j = 0; j < 4; j++)
@@ -503,6 +506,8 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraArg
           }
       }
     }
+    }
+  }
   }
 }
 

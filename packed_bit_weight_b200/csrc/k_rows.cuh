@@ -45,12 +45,25 @@ __device__ __forceinline__ int ld_dsmem_s32(const int* local, uint32_t r) {
 // pair's place.  ids outside [0, E) take no place; -1 says so on purpose
 // (padding, a request without an adapter), anything else raises the error.
 // With `rest` they are kept instead, as the last bin E - 1.
+//
+// RowTiles: the groups cut into tiles of at most T rows (equal ones of whole
+// 16-row steps), listed in group order, for kernels that give each tile a CTA.
 // ---------------------------------------------------------------------------
+struct RowTile {  // rows perm[start] .. perm[start + count - 1] of group g
+  int g, start, count, pad;
+};
+struct RowTiles {
+  RowTile* list;   // null: none wanted
+  int32_t* num;
+  int T;
+  int skip_last;   // the last bin gets no tiles
+};
+
 __host__ __device__ constexpr int route_rows_smem(int E) { return (kRowsSortWarps + 3) * E * 4; }
 
 __global__ void __launch_bounds__(kRowsSortThreads, 1)
     route_rows_kernel(const int32_t* __restrict__ ids, int P, int E, int rest, int32_t* __restrict__ offsets,
-                      int32_t* __restrict__ perm, int32_t* __restrict__ row_of) {
+                      int32_t* __restrict__ perm, int32_t* __restrict__ row_of, const RowTiles tiles) {
   extern __shared__ int smem_rows[];
   int* cnt = smem_rows;                      // [warp][E]: counts, then the warp's next place within its expert
   int* total = cnt + kRowsSortWarps * E;     // [E] this CTA's pairs per expert (read by the other CTAs)
@@ -100,23 +113,47 @@ __global__ void __launch_bounds__(kRowsSortThreads, 1)
     before[e] = b;
   }
   cluster_sync();  // (also: no CTA leaves while another still reads its totals)
-  if (warp == 0) {  // exclusive scan over the experts
-    int run = 0;
+  if (warp == 0) {  // exclusive scan over the experts, and over their tiles
+    const bool want = tiles.list && c == 0;
+    int run = 0, trun = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
-      const int v = e0 + lane < E ? grand[e0 + lane] : 0;
+      const int e = e0 + lane;
+      const int v = e < E ? grand[e] : 0;
       int s = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
         if (lane >= o) s += u;
       }
-      if (e0 + lane < E) {
-        grand[e0 + lane] = run + s - v;
-        if (c == 0) offsets[e0 + lane] = run + s - v;
+      if (e < E) {
+        grand[e] = run + s - v;
+        if (c == 0) offsets[e] = run + s - v;
       }
       run += __shfl_sync(0xFFFFFFFFu, s, 31);
+      if (want) {
+        const int t = (tiles.skip_last && e == E - 1) ? 0 : (v + tiles.T - 1) / tiles.T;
+        int ts = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xFFFFFFFFu, ts, o);
+          if (lane >= o) ts += u;
+        }
+        const int per = t ? (((v + t - 1) / t) + 15) & ~15 : 0;
+        for (int j = 0; j < t; j++) {
+          RowTile tile;
+          tile.g = e;
+          tile.count = max(0, min(per, v - j * per));
+          tile.pad = 0;
+          tile.start = grand[e] + j * per;
+          tiles.list[trun + ts - t + j] = tile;
+        }
+        trun += __shfl_sync(0xFFFFFFFFu, ts, 31);
+      }
     }
-    if (lane == 0 && c == 0) offsets[E] = run;
+    if (lane == 0 && c == 0) {
+      offsets[E] = run;
+      if (want) *tiles.num = trun;
+    }
   }
   __syncthreads();
   for (int i = 0; i < steps; i++) {

@@ -1358,7 +1358,7 @@ static int sort_ctas(int64_t P) {
 }
 
 static qmm_status launch_route_rows(const int32_t* ids, int64_t P, int64_t E, int rest, int32_t* offsets,
-                                    int32_t* perm, int32_t* row_of, cudaStream_t st) {
+                                    int32_t* perm, int32_t* row_of, const RowTiles& tiles, cudaStream_t st) {
   const int smem = route_rows_smem((int)E);
   if (smem > 48 * 1024 && cudaFuncSetAttribute(route_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                route_rows_smem(kRowsMaxBins + 1)) != cudaSuccess)
@@ -1376,7 +1376,7 @@ static qmm_status launch_route_rows(const int32_t* ids, int64_t P, int64_t E, in
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, route_rows_kernel, ids, (int)P, (int)E, rest, offsets, perm, row_of) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, route_rows_kernel, ids, (int)P, (int)E, rest, offsets, perm, row_of, tiles) != cudaSuccess)
     return QMM_ERR_CUDA;
   return launch_status();
 }
@@ -1393,7 +1393,7 @@ qmm_status qmm_route_rows(const int32_t* topk_ids, int64_t t, int64_t topk, int6
   DevInfo* di = nullptr;
   qmm_status s = device_info(&di);
   if (s != QMM_OK) return s;
-  s = launch_route_rows(topk_ids, P, num_experts, 0, expert_offsets, pair_perm, pair_row,
+  s = launch_route_rows(topk_ids, P, num_experts, 0, expert_offsets, pair_perm, pair_row, RowTiles{},
                         static_cast<cudaStream_t>(stream));
   if (s == QMM_OK) set_variant("route_rows<cluster=%d>", sort_ctas(P));
   return s;
@@ -1606,7 +1606,7 @@ static LoraWorkspace lora_workspace(const qmm_adapters* ad, int64_t m) {
   w.perm = align256(4 * (size_t)(ad->num_adapters + 2));
   w.num = w.perm + align256(4 * (size_t)m);
   w.tiles = w.num + 256;
-  w.h = w.tiles + align256(sizeof(LoraTile) * (size_t)lora_max_tiles(ad->num_adapters, m));
+  w.h = w.tiles + align256(sizeof(RowTile) * (size_t)lora_max_tiles(ad->num_adapters, m));
   w.bytes = w.h + align256(4 * (size_t)m * (size_t)ad->rank);
   return w;
 }
@@ -1654,8 +1654,8 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
   a.base = base;
   a.y = y;
   if (m <= kLoraTokenRows) {
-    // parts of n per row: a CTA per SM and no fewer than 64 outputs each
-    int64_t parts = std::max<int64_t>(1, di->sms / (kLoraCluster * m));
+    // parts of n per row: up to two CTAs an SM, no fewer than 64 outputs each
+    int64_t parts = std::max<int64_t>(1, 2 * di->sms / (kLoraCluster * m));
     parts = std::min(parts, std::max<int64_t>(1, ad->n / (64 * kLoraCluster)));
     if (launch_pdl(lora_token_kernel, dim3((unsigned)(m * parts * kLoraCluster)), dim3(kLoraThreads), 0, st, a,
                    (int)parts) != cudaSuccess)
@@ -1667,32 +1667,45 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
   a.offsets = reinterpret_cast<int32_t*>(base_ws + w.offsets);
   a.perm = reinterpret_cast<int32_t*>(base_ws + w.perm);
   a.num_tiles = reinterpret_cast<int32_t*>(base_ws + w.num);
-  a.tiles = reinterpret_cast<LoraTile*>(base_ws + w.tiles);
+  a.tiles = reinterpret_cast<RowTile*>(base_ws + w.tiles);
   a.h = reinterpret_cast<float*>(base_ws + w.h);
-  a.T = lora_tile_rows(m);
   const int64_t tiles = lora_max_tiles(ad->num_adapters, m);
-  if (tiles > 65535 || tiles * kLoraCluster > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
-  if ((s = launch_route_rows(adapter_ids, m, ad->num_adapters + 1, 1, a.offsets, a.perm, nullptr, st)) != QMM_OK)
-    return s;
-  if (launch_pdl(lora_tiles_kernel, dim3(1), dim3(256), 0, st, a) != cudaSuccess) return QMM_ERR_CUDA;
+  if (tiles * kLoraCluster > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
+  const RowTiles rt = {a.tiles, a.num_tiles, lora_tile_rows(m), base == y};
+  s = launch_route_rows(adapter_ids, m, ad->num_adapters + 1, 1, a.offsets, a.perm, nullptr, rt, st);
+  if (s != QMM_OK) return s;
+  // tiles that are likely there (the grids cover every tile there can be)
+  const int64_t likely = std::max<int64_t>(
+      1, std::min(tiles, (m + rt.T - 1) / rt.T + std::min<int64_t>(m / 16, ad->num_adapters)));
+  const int64_t blocks = (ad->rank + 63) / 64;
+  // CTAs that share a tile's k: as many as fill two CTAs an SM, at most 8
+  int cs = 8;
+  while (cs > 1 && likely * blocks * cs > 2 * di->sms) cs /= 2;
   const int shrink_smem = 128 * 64 * 4;  // 8 warps of 16 rows x 64 sums
-  if (cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shrink_smem) != cudaSuccess)
-    return QMM_ERR_CUDA;
-  if (launch_pdl(lora_shrink_kernel, dim3((unsigned)(tiles * kLoraCluster)), dim3(kLoraThreads), shrink_smem, st, a) !=
-      cudaSuccess)
-    return QMM_ERR_CUDA;
-  // columns: two CTAs an SM over the tiles that are likely there, whole 256-column steps
-  const int64_t likely = std::max<int64_t>(1, std::min(tiles, (m + a.T - 1) / a.T + std::min<int64_t>(m / 16, ad->num_adapters)));
-  int64_t cols = std::max<int64_t>(1, 2 * di->sms / likely);
-  cols = std::min(cols, (ad->n + 255) / 256);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * cs), (unsigned)blocks);
+  cfg.blockDim = dim3(kLoraThreads);
+  cfg.dynamicSmemBytes = shrink_smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cs;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, lora_shrink_kernel, a) != cudaSuccess) return QMM_ERR_CUDA;
   const int kc = (int)((ad->rank + 31) / 32), KC = kc <= 1 ? 1 : kc <= 2 ? 2 : kc <= 4 ? 4 : 8;
-  const int smem = (a.T / 16) * KC * 4 * 32 * 16;
+  const int smem = (rt.T / 16) * KC * 4 * 32 * 16;
   auto kern = KC == 1 ? lora_expand_kernel<1> : KC == 2 ? lora_expand_kernel<2> : KC == 4 ? lora_expand_kernel<4>
                                                                                          : lora_expand_kernel<8>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return QMM_ERR_CUDA;
-  if (launch_pdl(kern, dim3((unsigned)cols, (unsigned)tiles), dim3(kLoraThreads), (size_t)smem, st, a) != cudaSuccess)
+  const int grid = (KC <= 4 ? 2 : 1) * di->sms;  // the CTAs that are resident at once
+  if (launch_pdl(kern, dim3((unsigned)grid), dim3(kLoraThreads), (size_t)smem, st, a) != cudaSuccess)
     return QMM_ERR_CUDA;
-  set_variant("lora_tiled<rows=%d,chunks=%d,cols=%d>", a.T, KC, (int)cols);
+  set_variant("lora_tiled<rows=%d,cluster=%d,chunks=%d>", rt.T, cs, KC);
   return launch_status();
 }
 
