@@ -11,6 +11,7 @@
 // the adapters in use, x, base and y; the products are rank / (bytes) small,
 // so legacy MMAs straight from global memory, without staging, keep up.
 #pragma once
+#include "k_gemm.cuh"
 #include "k_gemv.cuh"
 #include "k_rows.cuh"
 
@@ -113,7 +114,7 @@ __device__ __forceinline__ void copy_span(uint16_t* __restrict__ y, const uint16
 // At one row all of it is latency: a launch, two dependent reads (the id, then
 // A), a cluster barrier.
 // ---------------------------------------------------------------------------
-__global__ void __cluster_dims__(kLoraCluster, 1, 1) __launch_bounds__(kLoraThreads)
+__global__ void __cluster_dims__(kLoraCluster, 1, 1) __launch_bounds__(kLoraThreads, 2)
     lora_token_kernel(const LoraArgs p, int parts) {
   __shared__ float red[kLoraWarps][kLoraMaxRank / kLoraCluster];
   __shared__ float mine[kLoraMaxRank / kLoraCluster];
@@ -169,11 +170,15 @@ __global__ void __cluster_dims__(kLoraCluster, 1, 1) __launch_bounds__(kLoraThre
 #pragma unroll 2
     for (int c = tid; c < k8; c += kLoraThreads) {
       const uint4 xv = xp[c];
+      uint4 w[8];  // (all loads before the first use)
 #pragma unroll
       for (int j = 0; j < 8; j++) {
         const int r = q * Rc + b + j;
-        if (b + j < Rc && r < rank) acc[j] = dot8(A[(int64_t)r * k8 + c], xv, acc[j]);
+        w[j] = (b + j < Rc && r < rank) ? A[(int64_t)r * k8 + c] : make_uint4(0u, 0u, 0u, 0u);
       }
+#pragma unroll
+      for (int j = 0; j < 8; j++)
+        if (b + j < Rc && q * Rc + b + j < rank) acc[j] = dot8(w[j], xv, acc[j]);
     }
 #pragma unroll
     for (int j = 0; j < 8; j++) {
@@ -231,65 +236,99 @@ __global__ void __cluster_dims__(kLoraCluster, 1, 1) __launch_bounds__(kLoraThre
 }
 
 // ---------------------------------------------------------------------------
-// Middle products of a tile: h[row][r] = sum_k A[r][k] x[row][k], fp32.  The
-// CTAs of a cluster each take a share of k (in whole 32-wide chunks), and in
-// a CTA the 8 warps are mw groups of 16 rows times 8/mw shares of that.  MMA
-// m16n8k16 with the rows as M and 64 of the ranks as N; the k order inside a
-// chunk is chosen so that a lane's 16 bytes of a row are its fragment words.
-// Partial sums meet in shared memory, then across the cluster, each in a fixed
-// order.
+// Middle products of a tile: h[row][r] = sum_k A[r][k] x[row][k], fp32, 64
+// ranks per CTA (blockIdx.y).  The CTAs of a cluster each take a share of k,
+// in blocks of 256: the block's piece of A arrives by cp.async in one of two
+// buffers (rows 576 bytes apart: the fragment reads of 8 rows hit every bank
+// group once) while the block before is multiplied, x comes straight from
+// global memory, each row read by one warp.  The 8 warps are mw groups of 16
+// rows times 8/mw shares of the block's eight 32-wide chunks.  MMA m16n8k16
+// with the rows as M and the ranks as N; the k order inside a chunk is chosen
+// so that a lane's 16 bytes of a row are its fragment words.  Partial sums
+// meet in shared memory, then across the cluster, each in a fixed order.
+// (With A read from global memory by every warp the loads of 8 rows' lines per
+// instruction took 38 us for 2,048 rows of rank 128 and k = 4096.)
 // ---------------------------------------------------------------------------
+constexpr int kShrinkK = 256;                       // k per block
+constexpr int kShrinkRow = kShrinkK * 2 + 64;       // bytes between rows of A in a buffer
+constexpr int kShrinkBuf = 64 * kShrinkRow;
+constexpr int kShrinkSmem = 2 * kShrinkBuf;         // (the partial sums, 32 KB, take the first buffer's place)
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool on) {
+  const uint32_t bytes = on ? 16u : 0u;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const LoraArgs p) {
-  extern __shared__ __align__(16) float sh[];  // [kw][mw * 16][64] partial sums, then [mw * 16][64] of this CTA
-  __shared__ int64_t xrow[128];
+  extern __shared__ __align__(16) uint8_t smem_shrink[];
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grp = lane >> 2, tig = lane & 3;
   const int q = (int)cluster_ctarank(), cs = (int)cluster_nctarank(), t = blockIdx.x / cs;
-  if (t >= *p.num_tiles) return;  // the whole cluster
-  const RowTile tile = p.tiles[t];
+  const RowTile tile = p.tiles[t];  // (the list has room for every CTA's tile)
+  if (t >= *p.num_tiles) return;    // the whole cluster
   if (tile.g >= p.L || tile.count <= 0) return;
-  const int rank = lora_rank(p, tile.g), R = p.R;
-  for (int i = tid; i < tile.count; i += kLoraThreads) xrow[i] = (int64_t)p.perm[tile.start + i] * p.k;
-  __syncthreads();
+  const int rank = lora_rank(p, tile.g), R = p.R, rb = blockIdx.y * 64;
   int mw = 1;
   while (mw * 16 < tile.count) mw *= 2;
   const int kw = kLoraWarps / mw;
   const int mg = warp % mw, ks = warp / mw;
-  const int chunks = (p.k + 31) >> 5, shares = cs * kw, share = q * kw + ks;
-  const int ch0 = (int)((int64_t)chunks * share / shares), ch1 = (int)((int64_t)chunks * (share + 1) / shares);
-  const int row0 = mg * 16 + grp, row1 = row0 + 8;
-  const uint16_t* x0 = p.x + (row0 < tile.count ? xrow[row0] : xrow[0]);
-  const uint16_t* x1 = p.x + (row1 < tile.count ? xrow[row1] : xrow[0]);
+  const int blocks = (p.k + kShrinkK - 1) / kShrinkK;
+  const int bl0 = blocks * q / cs, bl1 = blocks * (q + 1) / cs;
   const uint16_t* A = lora_a(p, tile.g);
+  const uint32_t sm = smem_addr(smem_shrink);
+  const int arow = tid >> 5, acol = tid & 31;  // 8 rows of 32 pieces per pass
+  auto stage = [&](int bl) {
+    const uint32_t dst = sm + (bl & 1) * kShrinkBuf + arow * kShrinkRow + acol * 16;
+    const int kk = bl * kShrinkK + acol * 8;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const int r = rb + arow + 8 * i;
+      const bool on = r < rank && kk < p.k;  // (k % 8 == 0: a piece is inside or outside)
+      cp_async16_zfill(dst + i * 8 * kShrinkRow, on ? A + (int64_t)r * p.k + kk : A, on);
+    }
+    cp_commit_g();
+  };
+  if (bl0 < bl1) stage(bl0);
+  const int row0 = mg * 16 + grp, row1 = row0 + 8;
+  const uint16_t* x0 = p.x + (int64_t)p.perm[tile.start + (row0 < tile.count ? row0 : 0)] * p.k;
+  const uint16_t* x1 = p.x + (int64_t)p.perm[tile.start + (row1 < tile.count ? row1 : 0)] * p.k;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  const int rb = blockIdx.y * 64;  // this CTA's block of ranks
-  const int nt = min(8, (R - rb) >> 3);
   float acc[8][4];
 #pragma unroll
   for (int j = 0; j < 8; j++)
 #pragma unroll
     for (int c = 0; c < 4; c++) acc[j][c] = 0.f;
-#pragma unroll 2
-  for (int ch = ch0; ch < ch1; ch++) {
-    const int kk = ch * 32 + tig * 8;
-    const bool in = kk < p.k;  // (k % 8 == 0: a piece is inside or outside)
-    const uint4 u0 = in ? *reinterpret_cast<const uint4*>(x0 + kk) : zero;
-    const uint4 u1 = in ? *reinterpret_cast<const uint4*>(x1 + kk) : zero;
-    uint4 w[8];
+  for (int bl = bl0; bl < bl1; bl++) {
+    if (bl + 1 < bl1) stage(bl + 1);
+    else cp_commit_g();  // (an empty group keeps the count)
+    uint4 u[8][2];  // this warp's chunks of the block
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-      w[j] = (in && j < nt && rb + 8 * j + grp < rank)
-                 ? *reinterpret_cast<const uint4*>(A + (int64_t)(rb + 8 * j + grp) * p.k + kk)
-                 : zero;
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      if (j >= nt) break;
-      mma_16816(acc[j], u0.x, u1.x, u0.y, u1.y, w[j].x, w[j].y);
-      mma_16816(acc[j], u0.z, u1.z, u0.w, u1.w, w[j].z, w[j].w);
+    for (int c = 0; c < 8; c++) {
+      const int kk = bl * kShrinkK + (ks * mw + c) * 32 + tig * 8;
+      const bool in = c < mw && kk < p.k;
+      u[c][0] = in ? *reinterpret_cast<const uint4*>(x0 + kk) : zero;
+      u[c][1] = in ? *reinterpret_cast<const uint4*>(x1 + kk) : zero;
     }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    const uint32_t src = sm + (bl & 1) * kShrinkBuf + grp * kShrinkRow + tig * 16 + ks * mw * 64;
+#pragma unroll
+    for (int c = 0; c < 8; c++) {
+      if (c >= mw) break;
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const uint4 w = lds128(src + c * 64 + 8 * j * kShrinkRow);
+        mma_16816(acc[j], u[c][0].x, u[c][1].x, u[c][0].y, u[c][1].y, w.x, w.y);
+        mma_16816(acc[j], u[c][0].z, u[c][1].z, u[c][0].w, u[c][1].w, w.z, w.w);
+      }
+    }
+    __syncthreads();  // the buffer may be filled again
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
   // partial sums [ks][row][64]
-  float* mine = sh + (int64_t)(ks * mw * 16) * 64;
+  float* sh = reinterpret_cast<float*>(smem_shrink);
+  float* mine = sh + (ks * mw * 16) * 64;
 #pragma unroll
   for (int j = 0; j < 8; j++) {
     const int c = 8 * j + 2 * tig;

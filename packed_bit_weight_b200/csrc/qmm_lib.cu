@@ -1587,9 +1587,15 @@ static qmm_status check_adapters(const qmm_adapters* ad) {
   return QMM_OK;
 }
 
-// Up to this many rows a cluster per row (lora_token_kernel): no sort, one
-// launch; above it the tiled path.
-constexpr int64_t kLoraTokenRows = 16;
+// A cluster per row (lora_token_kernel: no sort, one launch, A and B read once
+// per row) while that reads little, else the tiled path, which reads them once
+// per tile but has three launches.  On B200, us, cluster per row / tiled (rows
+// of four adapters): 32 rows, rank 16, 4096 -> 18560 (23 MB): 16.4 / 21.5; 16
+// rows of rank 64 (46 MB): 22.6 / 23.6; 24 (70 MB): 30.7 / 23.5; 64 rows of
+// rank 16: 24.6 / 23.6.
+static bool lora_by_row(const qmm_adapters* ad, int64_t m) {
+  return m <= 64 && m * ad->rank * (ad->n + ad->k) <= (int64_t)24 << 20;
+}
 
 // Rows per tile: B and A are read once per tile, so long inputs take large
 // ones; short ones small ones, for the number of CTAs.
@@ -1602,7 +1608,7 @@ struct LoraWorkspace {
 };
 static LoraWorkspace lora_workspace(const qmm_adapters* ad, int64_t m) {
   LoraWorkspace w = {};
-  if (m <= kLoraTokenRows || ad->rank == 0 || ad->k == 0) return w;
+  if (ad->rank == 0 || ad->k == 0 || lora_by_row(ad, m)) return w;
   w.perm = align256(4 * (size_t)(ad->num_adapters + 2));
   w.num = w.perm + align256(4 * (size_t)m);
   w.tiles = w.num + 256;
@@ -1653,9 +1659,11 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
   a.x = x;
   a.base = base;
   a.y = y;
-  if (m <= kLoraTokenRows) {
-    // parts of n per row: up to two CTAs an SM, no fewer than 64 outputs each
-    int64_t parts = std::max<int64_t>(1, 2 * di->sms / (kLoraCluster * m));
+  if (lora_by_row(ad, m)) {
+    // parts of n per row, no fewer than 64 outputs each: one CTA an SM up to
+    // four rows (every part computes the middle product again: at one row two
+    // an SM took 18.4 us, one 14.4), then two (16 rows 22.6 us, one 28.7)
+    int64_t parts = std::max<int64_t>(1, (m <= 4 ? 1 : 2) * di->sms / (kLoraCluster * m));
     parts = std::min(parts, std::max<int64_t>(1, ad->n / (64 * kLoraCluster)));
     if (launch_pdl(lora_token_kernel, dim3((unsigned)(m * parts * kLoraCluster)), dim3(kLoraThreads), 0, st, a,
                    (int)parts) != cudaSuccess)
@@ -1678,14 +1686,16 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
   const int64_t likely = std::max<int64_t>(
       1, std::min(tiles, (m + rt.T - 1) / rt.T + std::min<int64_t>(m / 16, ad->num_adapters)));
   const int64_t blocks = (ad->rank + 63) / 64;
-  // CTAs that share a tile's k: as many as fill two CTAs an SM, at most 8
+  // CTAs that share a tile's k: as many as fill two CTAs an SM (a little over
+  // is better than half), at most 8
   int cs = 8;
-  while (cs > 1 && likely * blocks * cs > 2 * di->sms) cs /= 2;
-  const int shrink_smem = 128 * 64 * 4;  // 8 warps of 16 rows x 64 sums
+  while (cs > 1 && likely * blocks * cs * 4 > 9 * di->sms) cs /= 2;
+  if (cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShrinkSmem) != cudaSuccess)
+    return QMM_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * cs), (unsigned)blocks);
   cfg.blockDim = dim3(kLoraThreads);
-  cfg.dynamicSmemBytes = shrink_smem;
+  cfg.dynamicSmemBytes = kShrinkSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
