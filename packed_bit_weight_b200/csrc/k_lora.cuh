@@ -372,28 +372,36 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
 // bits (off by 2^-22 where one fp16 would be off by 2^-12) at twice the MMAs,
 // which the stream of base and y hides.
 // ---------------------------------------------------------------------------
+// CTAs per SM: what the registers of B's fragments (16 KC a thread) leave
+constexpr int lora_expand_ctas(int KC) { return KC <= 4 ? 2 : 1; }
+
 template <int KC>  // 32-wide chunks of the rank: R <= 32 KC
-__global__ void __launch_bounds__(kLoraThreads, KC <= 4 ? 2 : 1) lora_expand_kernel(const LoraArgs p) {
+__global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expand_kernel(const LoraArgs p) {
   extern __shared__ __align__(16) uint4 frag[];  // [row group][chunk][step][hi, lo][lane] fragments of h
-  __shared__ int yrow[128];
-  __shared__ float pow2[128];
+  __shared__ int64_t yoff[128];  // rows of base and y, in elements
+  __shared__ float factor[128];  // s 2^e of each row
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grp = lane >> 2, tig = lane & 3;
-  // the tiles times as many column ranges as give every CTA of the grid one
-  // item (the number of tiles is known only here)
+  // The work is num tiles x nch pieces of 256 columns (32 a warp), tiles
+  // outer; every CTA takes an equal run of it, which is mostly one tile's (the
+  // number of tiles is known only here).
   const int num = *p.num_tiles, n = p.n, R = p.R;
-  const int cols = num > 0 ? min(max((int)gridDim.x / num, 1), (n + 255) / 256) : 1;
-  const int per = ((n + cols * 32 - 1) / (cols * 32)) * 32;
-  for (int item = blockIdx.x; item < num * cols; item += gridDim.x) {
-  const RowTile tile = p.tiles[item / cols];
-  const int c0 = (item % cols) * per, c1 = min(c0 + per, n);
-  if (tile.count <= 0 || c0 >= c1) continue;
+  const int nch = (n + 255) / 256;
+  const int64_t units = (int64_t)num * nch;
+  const int64_t u1 = units * (blockIdx.x + 1) / gridDim.x;
+  int run = 0;
+  for (int64_t u = units * blockIdx.x / gridDim.x; u < u1; u += run) {
+  const int t = (int)(u / nch), first = (int)(u - (int64_t)t * nch);
+  run = (int)min((int64_t)(nch - first), u1 - u);
+  const RowTile tile = p.tiles[t];
+  const int c0 = first * 256, c1 = min((first + run) * 256, n);
+  if (tile.count <= 0) continue;
   __syncthreads();  // (the last item's rows and fragments are no longer read)
-  for (int i = tid; i < tile.count; i += kLoraThreads) yrow[i] = p.perm[tile.start + i];
+  for (int i = tid; i < tile.count; i += kLoraThreads) yoff[i] = (int64_t)p.perm[tile.start + i] * n;
   if (tile.g >= p.L) {  // rows without an adapter
     __syncthreads();
     for (int i = warp; i < tile.count; i += kLoraWarps) {
-      const int64_t at = (int64_t)yrow[i] * n;
+      const int64_t at = yoff[i];
       copy_span(p.y + at, p.base + at, c0, c1, (n & 7) == 0, lane, 32);
     }
     continue;
@@ -401,17 +409,18 @@ __global__ void __launch_bounds__(kLoraThreads, KC <= 4 ? 2 : 1) lora_expand_ker
   const int rank = lora_rank(p, tile.g);
   const float scale = p.scales[tile.g];
   const int groups = (tile.count + 15) >> 4;
-  // fragments of h: two rows per warp at a time
-  for (int i0 = warp * 2; i0 < groups * 16; i0 += kLoraWarps * 2) {
-    float v[2][KC];
+  // fragments of h: kAtOnce rows per warp at a time
+  constexpr int kAtOnce = KC <= 4 ? 4 : 2;
+  for (int i0 = warp * kAtOnce; i0 < groups * 16; i0 += kLoraWarps * kAtOnce) {
+    float v[kAtOnce][KC];
 #pragma unroll
-    for (int r = 0; r < 2; r++)
+    for (int r = 0; r < kAtOnce; r++)
 #pragma unroll
       for (int c = 0; c < KC; c++)
         v[r][c] = (i0 + r < tile.count && 32 * c + lane < R) ? p.h[(int64_t)(tile.start + i0 + r) * R + 32 * c + lane]
                                                              : 0.f;
 #pragma unroll
-    for (int r = 0; r < 2; r++) {
+    for (int r = 0; r < kAtOnce; r++) {
     const int i = i0 + r;
     float top = 0.f;
 #pragma unroll
@@ -426,7 +435,7 @@ __global__ void __launch_bounds__(kLoraThreads, KC <= 4 ? 2 : 1) lora_expand_ker
     const int sh = top > 0.f ? min(14 - e, 126) : 0;
     const float f1 = __uint_as_float((uint32_t)(127 + (sh >> 1)) << 23);
     const float f2 = __uint_as_float((uint32_t)(127 + (sh - (sh >> 1))) << 23);
-    if (lane == 0) pow2[i] = __uint_as_float((uint32_t)(127 - sh) << 23);
+    if (lane == 0) factor[i] = scale * __uint_as_float((uint32_t)(127 - sh) << 23);
     // column r = 32 c + 8 t + 4 s + 2 w + b of row i: word (row half) + 2 w of lane (i % 8, t), step s of chunk c, half b
     const int t = lane >> 3, s = (lane >> 2) & 1, w = (lane >> 1) & 1, b = lane & 1;
     const int word = ((i >> 3) & 1) + 2 * w, to = ((i & 7) << 2) | t;
@@ -473,7 +482,7 @@ __global__ void __launch_bounds__(kLoraThreads, KC <= 4 ? 2 : 1) lora_expand_ker
       for (int h = 0; h < 2; h++) {
         const int i = g * 16 + grp + 8 * h;
         v[h] = (vec && i < tile.count && col < c1)
-                   ? *reinterpret_cast<const uint4*>(p.base + (int64_t)yrow[i] * n + col)
+                   ? *reinterpret_cast<const uint4*>(p.base + yoff[i] + col)
                    : zero;
       }
     };
@@ -492,7 +501,7 @@ __global__ void __launch_bounds__(kLoraThreads, KC <= 4 ? 2 : 1) lora_expand_ker
       if (g >= groups) break;
       const int i0 = g * 16 + grp, i1 = i0 + 8;
       const bool ok0 = i0 < tile.count, ok1 = i1 < tile.count;
-      const int64_t at0 = (int64_t)yrow[ok0 ? i0 : 0] * n + col, at1 = (int64_t)yrow[ok1 ? i1 : 0] * n + col;
+      const int64_t at0 = yoff[ok0 ? i0 : 0] + col, at1 = yoff[ok1 ? i1 : 0] + col;
       const uint4 b0 = ahead[d][0], b1 = ahead[d][1];
       load_base(g + kAhead, ahead[d]);
       float acc[4][4];
@@ -516,15 +525,15 @@ __global__ void __launch_bounds__(kLoraThreads, KC <= 4 ? 2 : 1) lora_expand_ker
         }
       }
       // acc[j][0..1]: row i0, columns col + 2j, + 1; acc[j][2..3]: row i1
-      const float q0 = pow2[i0], q1 = pow2[i1];
+      const float q0 = factor[i0], q1 = factor[i1];
       if (vec) {
         const uint32_t bw0[4] = {b0.x, b0.y, b0.z, b0.w}, bw1[4] = {b1.x, b1.y, b1.z, b1.w};
         uint32_t o0[4], o1[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) {
           const float2 f0 = f16x2_to_f32x2(bw0[j]), f1 = f16x2_to_f32x2(bw1[j]);
-          o0[j] = f32x2_to_f16x2(fmaf(scale, acc[j][0] * q0, f0.x), fmaf(scale, acc[j][1] * q0, f0.y));
-          o1[j] = f32x2_to_f16x2(fmaf(scale, acc[j][2] * q1, f1.x), fmaf(scale, acc[j][3] * q1, f1.y));
+          o0[j] = f32x2_to_f16x2(fmaf(acc[j][0], q0, f0.x), fmaf(acc[j][1], q0, f0.y));
+          o1[j] = f32x2_to_f16x2(fmaf(acc[j][2], q1, f1.x), fmaf(acc[j][3], q1, f1.y));
         }
         if (ok0 && col < c1) *reinterpret_cast<uint4*>(p.y + at0) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
         if (ok1 && col < c1) *reinterpret_cast<uint4*>(p.y + at1) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
@@ -536,11 +545,11 @@ __global__ void __launch_bounds__(kLoraThreads, KC <= 4 ? 2 : 1) lora_expand_ker
             if (col + 2 * j + b >= c1) continue;
             if (ok0) {
               const int64_t at = at0 + 2 * j + b;
-              p.y[at] = f32_to_f16_bits(fmaf(scale, acc[j][b] * q0, __half2float(__ushort_as_half(p.base[at]))));
+              p.y[at] = f32_to_f16_bits(fmaf(acc[j][b], q0, __half2float(__ushort_as_half(p.base[at]))));
             }
             if (ok1) {
               const int64_t at = at1 + 2 * j + b;
-              p.y[at] = f32_to_f16_bits(fmaf(scale, acc[j][b + 2] * q1, __half2float(__ushort_as_half(p.base[at]))));
+              p.y[at] = f32_to_f16_bits(fmaf(acc[j][b + 2], q1, __half2float(__ushort_as_half(p.base[at]))));
             }
           }
       }

@@ -1597,10 +1597,13 @@ static bool lora_by_row(const qmm_adapters* ad, int64_t m) {
   return m <= 64 && m * ad->rank * (ad->n + ad->k) <= (int64_t)24 << 20;
 }
 
-// Rows per tile: B and A are read once per tile, so long inputs take large
-// ones; short ones small ones, for the number of CTAs.
-static int lora_tile_rows(int64_t m) { return m >= 1024 ? 128 : m >= 512 ? 64 : 32; }
-static int64_t lora_max_tiles(int64_t L, int64_t m) { return m / lora_tile_rows(m) + std::min(m, L + 1); }
+// Rows per tile: A and B are read once per tile, so long inputs take larger
+// ones, short ones smaller, for the number of CTAs (2,048 rows of rank 128:
+// 128 rows a tile no faster than 64, middle products 27 us against 23).
+static int lora_tile_rows(int64_t m) { return m >= 512 ? 64 : 32; }
+static int64_t lora_max_tiles(int64_t L, int64_t m) {
+  return m / lora_tile_rows(m) + std::min(m, L + 1);
+}
 
 // Workspace of the tiled path: offsets, permutation, tile count, tiles, h.
 struct LoraWorkspace {
@@ -1682,14 +1685,11 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
   const RowTiles rt = {a.tiles, a.num_tiles, lora_tile_rows(m), base == y};
   s = launch_route_rows(adapter_ids, m, ad->num_adapters + 1, 1, a.offsets, a.perm, nullptr, rt, st);
   if (s != QMM_OK) return s;
-  // tiles that are likely there (the grids cover every tile there can be)
-  const int64_t likely = std::max<int64_t>(
-      1, std::min(tiles, (m + rt.T - 1) / rt.T + std::min<int64_t>(m / 16, ad->num_adapters)));
   const int64_t blocks = (ad->rank + 63) / 64;
-  // CTAs that share a tile's k: as many as fill two CTAs an SM (a little over
-  // is better than half), at most 8
+  // CTAs that share a tile's k: as many as fill two CTAs an SM if every tile
+  // there can be is there (a little over is better than half), at most 8
   int cs = 8;
-  while (cs > 1 && likely * blocks * cs * 4 > 9 * di->sms) cs /= 2;
+  while (cs > 1 && tiles * blocks * cs * 3 > 7 * di->sms) cs /= 2;
   if (cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShrinkSmem) != cudaSuccess)
     return QMM_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -1712,7 +1712,7 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
   auto kern = KC == 1 ? lora_expand_kernel<1> : KC == 2 ? lora_expand_kernel<2> : KC == 4 ? lora_expand_kernel<4>
                                                                                          : lora_expand_kernel<8>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return QMM_ERR_CUDA;
-  const int grid = (KC <= 4 ? 2 : 1) * di->sms;  // the CTAs that are resident at once
+  const int grid = lora_expand_ctas(KC) * di->sms;  // the CTAs that are resident at once
   if (launch_pdl(kern, dim3((unsigned)grid), dim3(kLoraThreads), (size_t)smem, st, a) != cudaSuccess)
     return QMM_ERR_CUDA;
   set_variant("lora_tiled<rows=%d,cluster=%d,chunks=%d>", rt.T, cs, KC);
