@@ -11,8 +11,7 @@
 // the adapters in use, x, base and y; the products are rank / (bytes) small,
 // so legacy MMAs straight from global memory, without staging, keep up.
 #pragma once
-#include "k_gemm.cuh"
-#include "k_gemv.cuh"
+#include "k_ggemm.cuh"
 #include "k_rows.cuh"
 
 namespace qmm {
@@ -372,6 +371,33 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
 // bits (off by 2^-22 where one fp16 would be off by 2^-12) at twice the MMAs,
 // which the stream of base and y hides.
 // ---------------------------------------------------------------------------
+// Scale of a row of h held 32 values per register across the warp: f1 f2 =
+// 2^(14 - e) for the largest finite |value| in [2^e, 2^(e+1)) (two factors, so
+// that neither leaves fp32), back = 2^(e - 14).
+template <int N>
+__device__ __forceinline__ void h_scale(const float (&v)[N], float& f1, float& f2, float& back) {
+  float top = 0.f;
+#pragma unroll
+  for (int c = 0; c < N; c++) {
+    const float f = fabsf(v[c]);
+    if (f <= 3.4028235e38f) top = fmaxf(top, f);  // (finite)
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const int e = (int)(__float_as_uint(top) >> 23) - 127;
+  const int sh = top > 0.f ? min(14 - e, 126) : 0;
+  f1 = __uint_as_float((uint32_t)(127 + (sh >> 1)) << 23);
+  f2 = __uint_as_float((uint32_t)(127 + (sh - (sh >> 1))) << 23);
+  back = __uint_as_float((uint32_t)(127 - sh) << 23);
+}
+// x = hi + lo (+ 2^-22 |x|) as fp16 halves; an infinite or NaN hi has lo = 0.
+__device__ __forceinline__ void h_split(float x, uint16_t& hi, uint16_t& lo) {
+  const __half h = __float2half_rn(x);
+  const float back = __half2float(h);
+  hi = __half_as_ushort(h);
+  lo = fabsf(back) <= 65504.f ? __half_as_ushort(__float2half_rn(x - back)) : (uint16_t)0;
+}
+
 // CTAs per SM: what the registers of B's fragments (16 KC a thread) leave
 constexpr int lora_expand_ctas(int KC) { return KC <= 4 ? 2 : 1; }
 
@@ -422,31 +448,17 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
 #pragma unroll
     for (int r = 0; r < kAtOnce; r++) {
     const int i = i0 + r;
-    float top = 0.f;
-#pragma unroll
-    for (int c = 0; c < KC; c++) {
-      const float f = fabsf(v[r][c]);
-      if (f <= 3.4028235e38f) top = fmaxf(top, f);  // (finite)
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    // top in [2^e, 2^(e+1)): scaled by 2^(14 - e), in two factors so that neither leaves fp32
-    const int e = (int)(__float_as_uint(top) >> 23) - 127;
-    const int sh = top > 0.f ? min(14 - e, 126) : 0;
-    const float f1 = __uint_as_float((uint32_t)(127 + (sh >> 1)) << 23);
-    const float f2 = __uint_as_float((uint32_t)(127 + (sh - (sh >> 1))) << 23);
-    if (lane == 0) factor[i] = scale * __uint_as_float((uint32_t)(127 - sh) << 23);
+    float f1, f2, back;
+    h_scale<KC>(v[r], f1, f2, back);
+    if (lane == 0) factor[i] = scale * back;
     // column r = 32 c + 8 t + 4 s + 2 w + b of row i: word (row half) + 2 w of lane (i % 8, t), step s of chunk c, half b
     const int t = lane >> 3, s = (lane >> 2) & 1, w = (lane >> 1) & 1, b = lane & 1;
     const int word = ((i >> 3) & 1) + 2 * w, to = ((i & 7) << 2) | t;
 #pragma unroll
     for (int c = 0; c < KC; c++) {
-      const float x = v[r][c] * f1 * f2;
-      const __half hi = __float2half_rn(x);
-      const float back = __half2float(hi);
-      const bool finite = fabsf(back) <= 65504.f;
-      const __half lo = finite ? __float2half_rn(x - back) : __float2half_rn(0.f);
-      __half* f = reinterpret_cast<__half*>(frag + ((((i >> 4) * KC + c) * 2 + s) * 2) * 32 + to);
+      uint16_t hi, lo;
+      h_split(v[r][c] * f1 * f2, hi, lo);
+      uint16_t* f = reinterpret_cast<uint16_t*>(frag + ((((i >> 4) * KC + c) * 2 + s) * 2) * 32 + to);
       f[word * 2 + b] = hi;
       f[32 * 8 + word * 2 + b] = lo;
     }
@@ -556,6 +568,341 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
     }
     }
   }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The same for long inputs (tiles of up to 128 rows, R <= 128) on
+// 5th-generation tensor cores.  The tile's rows are M, 128 columns of y (rows of
+// B, brought by TMA into 128-byte-swizzled stages) are N, and K runs over the
+// rank twice, for the two halves of h, against the same stage of B.  A lane of
+// the epilogue then holds a row's neighbouring columns, 32 bytes a load and
+// store (with the columns as M it held a column, and the exchange between lanes
+// alone was 3/4 of 75 us).  The legacy MMAs of lora_expand_kernel take 34 us of tensor time
+// alone at 2,048 rows of rank 128 and 18,560 columns and their fragments as
+// much again; here the products take 9 us and the stream of base and y is what
+// remains.
+//
+// Roles (one CTA per SM, an equal run of (tile, 128 columns) units each):
+//   warp 0       B by TMA, kLtStages deep
+//   warp 1       tcgen05.mma issue; owns tensor memory (4 accumulators of 128
+//                columns)
+//   warps 2-3    zero what a rank that is not a multiple of 16 leaves of its
+//                last 16 columns in each stage (it may hold anything)
+//   warps 4-11   write a tile's h into shared memory when the tile changes;
+//                epilogue: warps 4-7 the even units, 8-11 the odd ones, with
+//                base loaded before the wait for the products
+// Every wait is bounded, as in the GEMMs.
+// ---------------------------------------------------------------------------
+constexpr int kLtStages = 3, kLtThreads = 12 * 32, kLtEpi = 8 * 32;
+constexpr int kLtHalf = 128 * 128;               // bytes of 128 rows x 64 k
+__host__ __device__ constexpr int lora_tc_smem(int KB) {
+  return 1024 + 2 * KB * kLtHalf + kLtStages * KB * kLtHalf + 256;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// Ranks whose last k16 step is not all of their own columns.
+__device__ __forceinline__ bool lora_partial(int rank) { return (rank & 15) != 0 || rank == 0; }
+
+// 32 bytes a lane (32-byte aligned).
+__device__ __forceinline__ void ld256(uint32_t (&w)[8], const void* p) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st256(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+template <int KB>  // 64-wide k blocks: R <= 64 KB
+__global__ void __launch_bounds__(kLtThreads, 1)
+    lora_expand_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ LoraArgs p) {
+  extern __shared__ uint8_t smem_lt[];
+  __shared__ int64_t yoff[2][128];
+  __shared__ float factor[2][128];
+  __shared__ volatile int s_abort;
+  const uint32_t base = (smem_addr(smem_lt) + 1023u) & ~1023u;
+  const uint32_t h_s = base, b_s = h_s + 2 * KB * kLtHalf, bars = b_s + kLtStages * KB * kLtHalf;
+  const uint32_t full = bars, fixd = full + 8 * kLtStages, empty = fixd + 8 * kLtStages, accf = empty + 8 * kLtStages,
+                 acce = accf + 32, hfree = acce + 32, hfull = hfree + 8, done_bar = hfull + 8, tmem_slot = done_bar + 8;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    s_abort = 0;
+    for (int s = 0; s < kLtStages; s++) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(fixd + 8 * s, 2);
+      mbar_init(empty + 8 * s, 1);
+    }
+    for (int a = 0; a < 4; a++) {
+      mbar_init(accf + 8 * a, 1);
+      mbar_init(acce + 8 * a, 4);
+    }
+    mbar_init(hfree, 8);
+    mbar_init(hfull, 8);
+    mbar_init(done_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_enter();
+  uint32_t tmem;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
+  const int num = *p.num_tiles, n = p.n, R = p.R;
+  const int nch = (n + 127) >> 7;
+  const int64_t units = (int64_t)num * nch;
+  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  // (units of rows without an adapter are copied by the epilogue warps alone)
+
+  if (warp == 0) {
+    // ------------------------------- B -------------------------------------
+    if (lane == 0) {
+      prefetch_tmap(&tm_b);
+      uint32_t c = 0, issued = 0;  // stages filled
+      const bool withhold = (g_test_flags & kTestWithholdXTiles) != 0;  // test switch: issue nothing
+      for (int64_t u = u0; u < u1 && !withhold; u++) {
+        const int t = (int)(u / nch), ch = (int)(u - (int64_t)t * nch);
+        const RowTile tile = p.tiles[t];
+        if (tile.g >= p.L || tile.count <= 0) continue;
+        const uint32_t s = c % kLtStages;
+        if (!gg_wait(empty + 8 * s, ((c / kLtStages) & 1u) ^ 1u)) { s_abort = 1; break; }
+        mbar_arrive_expect_tx(full + 8 * s, KB * kLtHalf);
+        for (int b = 0; b < KB; b++)
+          tma_load_3d(b_s + (s * KB + b) * kLtHalf, &tm_b, b * 64, ch * 128, tile.g, full + 8 * s);
+        c++;
+        issued = c;
+      }
+      for (uint32_t s = 0; s < kLtStages && s < issued; s++) {  // drain our copies
+        const uint32_t last = issued - 1 - ((issued - 1 - s) % kLtStages);
+        gg_wait(full + 8 * s, (last / kLtStages) & 1u);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------- MMA issuer ------------------------------
+    const bool leader = elect_one();
+    uint32_t c = 0, tiles = 0;
+    int told = -1, rank = 0;
+    for (int64_t u = u0; u < u1; u++) {
+      const int t = (int)(u / nch);
+      const RowTile tile = p.tiles[t];
+      if (tile.g >= p.L || tile.count <= 0) continue;
+      bool ok = true;
+      if (t != told) {
+        rank = (int)warp_uniform((uint32_t)lora_rank(p, tile.g));
+        ok = gg_wait(hfull, tiles++ & 1u);
+        told = t;
+      }
+      const uint32_t s = c % kLtStages, a = c & 3u;
+      ok = ok && gg_wait(acce + 8 * a, ((c >> 2) & 1u) ^ 1u) && gg_wait(full + 8 * s, (c / kLtStages) & 1u);
+      if (lora_partial(rank)) ok = ok && gg_wait(fixd + 8 * s, (c / kLtStages) & 1u);
+      if (!__all_sync(0xFFFFFFFFu, ok)) { s_abort = 1; break; }
+      tc_fence_after();
+      const uint32_t idesc = umma_idesc_f16(128);
+      const uint32_t d = warp_uniform(tmem) + 128u * a;
+      const int k16 = max((rank + 15) >> 4, 1);  // (rank 0: one step of zeros)
+      if (leader) {
+        for (int kk = 0; kk < k16; kk++) {
+          const uint32_t blk = (uint32_t)(kk >> 2) * kLtHalf;
+          const uint64_t db = umma_desc_k128(b_s + s * KB * kLtHalf + blk) + (uint64_t)(2 * (kk & 3));
+          const uint64_t dh = umma_desc_k128(h_s + blk) + (uint64_t)(2 * (kk & 3));
+          umma_f16(d, dh, db, idesc, kk != 0);
+          umma_f16(d, dh + (uint64_t)(KB * kLtHalf / 16), db, idesc, 1);
+        }
+        umma_commit(empty + 8 * s);
+        umma_commit(accf + 8 * a);
+      }
+      __syncwarp();
+      c++;
+    }
+    if (leader) umma_commit(done_bar);
+  } else if (warp < 4) {
+    // ----------------------- ranks inside a k16 step ------------------------
+    uint32_t c = 0;
+    for (int64_t u = u0; u < u1; u++) {
+      const RowTile tile = p.tiles[u / nch];
+      if (tile.g >= p.L || tile.count <= 0) continue;
+      const int rank = lora_rank(p, tile.g);
+      const uint32_t s = c % kLtStages;
+      // (waits for every stage, needed or not: the barrier's phases keep pace)
+      const bool ok = gg_wait(full + 8 * s, (c / kLtStages) & 1u);
+      if (!__all_sync(0xFFFFFFFFu, ok)) { s_abort = 1; break; }
+      if (lora_partial(rank)) {
+        const int top = max((rank + 15) & ~15, 16);
+        for (int r = (warp - 2) * 64 + lane; r < (warp - 1) * 64; r += 32)
+          for (int k = rank; k < top; k++) {
+            const uint32_t at = b_s + (s * KB + (k >> 6)) * kLtHalf + r * 128 + ((((k & 63) >> 3) ^ (r & 7)) << 4) +
+                                (k & 7) * 2;
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)0) : "memory");
+          }
+        fence_proxy_async_shared();
+      }
+      warp_arrive(fixd + 8 * s, lane);
+      c++;
+    }
+  } else {
+    // -------------------------- h and epilogue ------------------------------
+    const int ew = warp - 4, q = warp & 3, grp = ew >> 2;
+    const bool vec = (n & 7) == 0;
+    // whole 32-byte sectors a lane where rows and buffers allow it
+    const bool wide = (n & 15) == 0 &&
+                      ((reinterpret_cast<uintptr_t>(p.base) | reinterpret_cast<uintptr_t>(p.y)) & 31) == 0;
+    const int row = 32 * q + lane;  // of the tile: a TMEM lane
+    uint32_t c = 0, tiles = 0;
+    int told = -1, tb = 0;
+    float scale = 0.f;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok; u++) {
+      const int t = (int)(u / nch), ch = (int)(u - (int64_t)t * nch);
+      const RowTile tile = p.tiles[t];
+      if (tile.count <= 0) continue;
+      if (tile.g >= p.L) {  // rows without an adapter
+        const int c0 = ch * 128, c1 = min(c0 + 128, n);
+        for (int i = ew; i < tile.count; i += 8) {
+          const int64_t at = (int64_t)p.perm[tile.start + i] * n;
+          copy_span(p.y + at, p.base + at, c0, c1, vec, lane, 32);
+        }
+        continue;
+      }
+      if (t != told) {
+        // a new tile: once every epilogue warp is here, all units of the last one
+        // have been multiplied (each has waited for that tile's last unit)
+        warp_arrive(hfree, lane);
+        ok = gg_wait(hfree, tiles & 1u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) { s_abort = 1; break; }
+        told = t;
+        tb ^= 1;
+        scale = p.scales[tile.g];
+        for (int i = tid - 128; i < tile.count; i += kLtEpi) yoff[tb][i] = (int64_t)p.perm[tile.start + i] * n;
+        for (int i0 = ew * 4; i0 < 128; i0 += 32) {
+          float v[4][2 * KB];
+#pragma unroll
+          for (int r = 0; r < 4; r++)
+#pragma unroll
+            for (int b = 0; b < 2 * KB; b++)
+              v[r][b] = (i0 + r < tile.count && 32 * b + lane < R)
+                            ? p.h[(int64_t)(tile.start + i0 + r) * R + 32 * b + lane]
+                            : 0.f;
+#pragma unroll
+          for (int r = 0; r < 4; r++) {
+            float f1, f2, back;
+            h_scale<2 * KB>(v[r], f1, f2, back);
+            const int i = i0 + r;
+            if (lane == 0) factor[tb][i] = scale * back;
+#pragma unroll
+            for (int b = 0; b < 2 * KB; b++) {
+              uint16_t hi, lo;
+              h_split(v[r][b] * f1 * f2, hi, lo);
+              const int k = 32 * b + lane;
+              const uint32_t at = h_s + (k >> 6) * kLtHalf + i * 128 + ((((k & 63) >> 3) ^ (i & 7)) << 4) + (k & 7) * 2;
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(hi) : "memory");
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + KB * kLtHalf), "h"(lo) : "memory");
+            }
+          }
+        }
+        fence_proxy_async_shared();
+        warp_arrive(hfull, lane);
+        ok = gg_wait(hfull, tiles++ & 1u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) { s_abort = 1; break; }
+      }
+      if ((int)(c & 1u) == grp) {
+        const uint32_t a = c & 3u;
+        const int c0 = ch * 128, left = n - c0;  // columns from here on
+        const bool live = row < tile.count;
+        const uint16_t* bp = p.base + yoff[tb][live ? row : 0] + c0;
+        uint16_t* yp = p.y + yoff[tb][live ? row : 0] + c0;
+        const float f = factor[tb][row];
+        // base, loaded before the products are waited for
+        uint32_t bv[4][16];
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+          for (int i = 0; i < 2; i++) {
+            uint32_t(&w)[8] = *reinterpret_cast<uint32_t(*)[8]>(&bv[j][8 * i]);
+            const int c = 32 * j + 16 * i;
+            if (live && wide && c < left) {
+              ld256(w, bp + c);
+            } else if (live && vec && c < left) {
+              const uint4 v0 = *reinterpret_cast<const uint4*>(bp + c);
+              const uint4 v1 = c + 8 < left ? *reinterpret_cast<const uint4*>(bp + c + 8) : make_uint4(0u, 0u, 0u, 0u);
+              w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w; w[4] = v1.x; w[5] = v1.y; w[6] = v1.z; w[7] = v1.w;
+            } else {
+#pragma unroll
+              for (int x = 0; x < 8; x++) w[x] = 0u;
+            }
+          }
+        ok = gg_wait(accf + 8 * a, (c >> 2) & 1u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) { s_abort = 1; break; }
+        tc_fence_after();
+        if (32 * q < tile.count) {
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            uint32_t r[32];
+            tmem_ld32(tmem + 128u * a + 32u * j + ((uint32_t)(32 * q) << 16), r);
+            tmem_ld_wait();
+            if (!live) continue;
+            if (vec) {
+#pragma unroll
+              for (int i = 0; i < 2; i++) {
+                const int c = 32 * j + 16 * i;
+                uint32_t o[8];
+#pragma unroll
+                for (int x = 0; x < 8; x++) {
+                  const float2 b = f16x2_to_f32x2(bv[j][8 * i + x]);
+                  o[x] = f32x2_to_f16x2(fmaf(__uint_as_float(r[16 * i + 2 * x]), f, b.x),
+                                        fmaf(__uint_as_float(r[16 * i + 2 * x + 1]), f, b.y));
+                }
+                if (wide) {
+                  if (c < left) st256(yp + c, o);
+                } else {
+                  if (c < left) *reinterpret_cast<uint4*>(yp + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                  if (c + 8 < left) *reinterpret_cast<uint4*>(yp + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < 32; x++)
+                if (32 * j + x < left)
+                  yp[32 * j + x] = f32_to_f16_bits(
+                      fmaf(__uint_as_float(r[x]), f, __half2float(__ushort_as_half(bp[32 * j + x]))));
+            }
+          }
+        }
+        tc_fence_before();
+        warp_arrive(acce + 8 * a, lane);
+      } else if (u + 1 == u1 || (u + 1) / nch != t) {
+        // the tile's last unit is the other group's: wait for its products too,
+        // so that h may be written again
+        ok = gg_wait(accf + 8 * (c & 3u), (c >> 2) & 1u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) { s_abort = 1; break; }
+      }
+      c++;
+    }
+  }
+
+  // teardown: no MMA of ours may still be using tensor memory
+  if (warp == 1 && lane == 0) gg_wait(done_bar, 0);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 

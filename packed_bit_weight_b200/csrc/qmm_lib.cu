@@ -137,6 +137,20 @@ static bool make_map_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt
   return r == CUDA_SUCCESS;
 }
 
+// 3-D map over [outer] stacks, outer_stride bytes apart, of row-major [rows][cols].
+static bool make_map_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int elem, uint64_t cols,
+                        uint64_t rows, uint64_t outer, uint64_t outer_stride, uint32_t box_cols, uint32_t box_rows,
+                        CUtensorMapSwizzle sw) {
+  if (!get_encoder()) return false;
+  cuuint64_t dims[3] = {cols, rows, outer};
+  cuuint64_t strides[2] = {cols * (uint64_t)elem, outer_stride};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // Launch with programmatic dependent launch (the kernel waits on the previous
 // one with griddepcontrol.wait before touching its outputs).
 template <typename... KArgs, typename... Args>
@@ -1598,11 +1612,12 @@ static bool lora_by_row(const qmm_adapters* ad, int64_t m) {
 }
 
 // Rows per tile: A and B are read once per tile, so long inputs take larger
-// ones, short ones smaller, for the number of CTAs (2,048 rows of rank 128:
-// 128 rows a tile no faster than 64, middle products 27 us against 23).
-static int lora_tile_rows(int64_t m) { return m >= 512 ? 64 : 32; }
-static int64_t lora_max_tiles(int64_t L, int64_t m) {
-  return m / lora_tile_rows(m) + std::min(m, L + 1);
+// ones, short ones smaller, for the number of CTAs.  From 512 rows of rank up
+// to 128 the expanding product runs on tcgen05 (lora_expand_tc_kernel).
+static bool lora_tc(int64_t m, int64_t rank) { return m >= 512 && rank <= 128; }
+static int lora_tile_rows(int64_t m, int64_t rank) { return lora_tc(m, rank) ? 128 : m >= 512 ? 64 : 32; }
+static int64_t lora_max_tiles(int64_t L, int64_t m, int64_t rank) {
+  return m / lora_tile_rows(m, rank) + std::min(m, L + 1);
 }
 
 // Workspace of the tiled path: offsets, permutation, tile count, tiles, h.
@@ -1615,7 +1630,7 @@ static LoraWorkspace lora_workspace(const qmm_adapters* ad, int64_t m) {
   w.perm = align256(4 * (size_t)(ad->num_adapters + 2));
   w.num = w.perm + align256(4 * (size_t)m);
   w.tiles = w.num + 256;
-  w.h = w.tiles + align256(sizeof(RowTile) * (size_t)lora_max_tiles(ad->num_adapters, m));
+  w.h = w.tiles + align256(sizeof(RowTile) * (size_t)lora_max_tiles(ad->num_adapters, m, ad->rank));
   w.bytes = w.h + align256(4 * (size_t)m * (size_t)ad->rank);
   return w;
 }
@@ -1680,9 +1695,9 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
   a.num_tiles = reinterpret_cast<int32_t*>(base_ws + w.num);
   a.tiles = reinterpret_cast<RowTile*>(base_ws + w.tiles);
   a.h = reinterpret_cast<float*>(base_ws + w.h);
-  const int64_t tiles = lora_max_tiles(ad->num_adapters, m);
+  const int64_t tiles = lora_max_tiles(ad->num_adapters, m, ad->rank);
   if (tiles * kLoraCluster > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
-  const RowTiles rt = {a.tiles, a.num_tiles, lora_tile_rows(m), base == y};
+  const RowTiles rt = {a.tiles, a.num_tiles, lora_tile_rows(m, ad->rank), base == y};
   s = launch_route_rows(adapter_ids, m, ad->num_adapters + 1, 1, a.offsets, a.perm, nullptr, rt, st);
   if (s != QMM_OK) return s;
   const int64_t blocks = (ad->rank + 63) / 64;
@@ -1707,6 +1722,21 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, lora_shrink_kernel, a) != cudaSuccess) return QMM_ERR_CUDA;
+  if (lora_tc(m, ad->rank)) {
+    CUtensorMap tb;
+    if (!make_map_3d(&tb, ad->b, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, (uint64_t)ad->rank, (uint64_t)ad->n,
+                     (uint64_t)ad->num_adapters, ad->num_adapters > 1 ? (uint64_t)ad->b_stride : align256(2 * (size_t)(ad->rank * ad->n)),
+                     64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+      return QMM_ERR_CUDA;
+    const int KB = ad->rank <= 64 ? 1 : 2;
+    auto tk = KB == 1 ? lora_expand_tc_kernel<1> : lora_expand_tc_kernel<2>;
+    if (cudaFuncSetAttribute(tk, cudaFuncAttributeMaxDynamicSharedMemorySize, lora_tc_smem(KB)) != cudaSuccess)
+      return QMM_ERR_CUDA;
+    if (launch_pdl(tk, dim3((unsigned)di->sms), dim3(kLtThreads), (size_t)lora_tc_smem(KB), st, tb, a) != cudaSuccess)
+      return QMM_ERR_CUDA;
+    set_variant("lora_tc<rows=%d,cluster=%d,blocks=%d>", rt.T, cs, KB);
+    return launch_status();
+  }
   const int kc = (int)((ad->rank + 31) / 32), KC = kc <= 1 ? 1 : kc <= 2 ? 2 : kc <= 4 ? 4 : 8;
   const int smem = (rt.T / 16) * KC * 4 * 32 * 16;
   auto kern = KC == 1 ? lora_expand_kernel<1> : KC == 2 ? lora_expand_kernel<2> : KC == 4 ? lora_expand_kernel<4>

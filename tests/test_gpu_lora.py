@@ -49,7 +49,8 @@ CASES = [  # m, n, k, R, L, how ids are drawn
     (16, 4096, 2048, 64, 16, "distinct"), (16, 999, 136, 40, 2, "any"), (17, 130, 896, 128, 5, "any"),
     (33, 520, 264, 8, 40, "any"), (64, 777, 512, 96, 1, "one"), (70, 264, 2560, 256, 3, "runs"),
     (128, 1024, 256, 16, 130, "distinct"), (300, 1096, 904, 64, 7, "runs"), (513, 260, 1024, 48, 9, "any"),
-    (1100, 333, 384, 128, 2, "runs")]
+    (1100, 333, 384, 128, 2, "runs"), (600, 1000, 256, 8, 3, "any"), (1500, 640, 128, 40, 30, "runs"),
+    (777, 129, 64, 72, 300, "any"), (520, 4104, 128, 120, 1, "one"), (640, 256, 64, 136, 3, "any")]
 
 
 def _ids(rng, m, L, how):
@@ -79,7 +80,7 @@ def test_lora(m, n, k, R, L, how, ranks):
     assert torch.equal(y2, y)                  # in place, and the same bits again
 
 
-@pytest.mark.parametrize("m", [1, 9, 100, 700])
+@pytest.mark.parametrize("m", [1, 9, 100, 300, 700])
 def test_bad_ids_and_ranks_are_reported(m):
     rng = np.random.default_rng(m)
     A, B, sc, _ = _pool(rng, 3, 16, 72, 64)
@@ -96,7 +97,7 @@ def test_bad_ids_and_ranks_are_reported(m):
     within(y.cpu().numpy(), *lora(_d(x), _d(base), ids, _d(A), _d(B), sc, rk))
 
 
-@pytest.mark.parametrize("m", [2, 40])
+@pytest.mark.parametrize("m", [2, 70, 600])
 def test_values_outside_fp16_between_the_products(m):
     """A x beyond fp16's range and below its smallest step, brought back by B
     and the scale: the middle product is held in fp32."""
@@ -114,7 +115,7 @@ def test_values_outside_fp16_between_the_products(m):
     within(y.cpu().numpy(), *lora(_d(x), _d(base), ids, _d(A), _d(B), sc, None))
 
 
-@pytest.mark.parametrize("m", [2, 40, 300])
+@pytest.mark.parametrize("m", [2, 40, 300, 700])
 def test_infinities_and_nan_stay_in_their_row(m):
     rng = np.random.default_rng(4)
     A, B, sc, _ = _pool(rng, 2, 32, 136, 256)
@@ -133,7 +134,7 @@ def test_infinities_and_nan_stay_in_their_row(m):
 def test_an_infinite_middle_product_gives_what_fp32_gives():
     """An infinity in x: A x is +-inf, and the outputs are +-inf or NaN where
     infinities of both signs (or 0 * inf) meet."""
-    for m in (1, 40):
+    for m in (1, 70, 600):
         L, R, n, k = 1, 8, 16, 64
         A, B = np.ones((L, R, k), np.float16), np.ones((L, n, R), np.float16)
         B[0, 1] = -1
@@ -155,7 +156,7 @@ def test_strided_pool():
     big_a[:, :16], big_b[:, :72] = A, B
     ad = qmm.Adapters(torch.from_numpy(big_a).cuda()[:, :16], torch.from_numpy(big_b).cuda()[:, :72],
                       torch.from_numpy(sc).cuda())
-    for m in (3, 50):
+    for m in (3, 70, 600):
         x, base = rng.standard_normal((m, 64)).astype(np.float16), rng.standard_normal((m, 72)).astype(np.float16)
         ids = _ids(rng, m, 4, "any")
         within(_run(ad, x, ids, base).cpu().numpy(), *lora(_d(x), _d(base), ids, _d(A), _d(B), sc, None))
@@ -170,14 +171,14 @@ def test_zero_sizes():
                  torch.empty(0, dtype=torch.int32, device="cuda"), e, e)
     for R, k in ((0, 64), (16, 0)):            # an empty sum: y = base
         A, B, sc, _ = _pool(rng, 2, R, 72, k)
-        for m in (3, 40):
+        for m in (3, 70, 600):
             base = rng.standard_normal((m, 72)).astype(np.float16)
             y = _run(_adapters(A, B, sc, None), np.zeros((m, k), np.float16), _ids(rng, m, 2, "any"), base)
             assert np.array_equal(y.cpu().numpy(), base)
     assert qmm.qmm_sync_check() == 0
 
 
-@pytest.mark.parametrize("m", [4, 200])
+@pytest.mark.parametrize("m", [4, 200, 530])
 def test_beside_a_packed_projection_on_two_streams_and_in_a_graph(m):
     """The projection and its adapters in place, as a server runs them: on two
     streams at once with a workspace each, and captured and replayed."""
