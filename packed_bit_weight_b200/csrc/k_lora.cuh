@@ -589,12 +589,12 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
 //                columns)
 //   warps 2-3    zero what a rank that is not a multiple of 16 leaves of its
 //                last 16 columns in each stage (it may hold anything)
-//   warps 4-11   write a tile's h into shared memory when the tile changes;
-//                epilogue: warps 4-7 the even units, 8-11 the odd ones, with
-//                base loaded before the wait for the products
+//   warps 4-19   write a tile's h into shared memory when the tile changes;
+//                epilogue: four groups of four warps take the units in turn,
+//                with base loaded before the wait for the products
 // Every wait is bounded, as in the GEMMs.
 // ---------------------------------------------------------------------------
-constexpr int kLtStages = 3, kLtThreads = 12 * 32, kLtEpi = 8 * 32;
+constexpr int kLtStages = 3, kLtGroups = 4, kLtEpi = kLtGroups * 4 * 32, kLtThreads = 4 * 32 + kLtEpi;
 constexpr int kLtHalf = 128 * 128;               // bytes of 128 rows x 64 k
 __host__ __device__ constexpr int lora_tc_smem(int KB) {
   return 1024 + 2 * KB * kLtHalf + kLtStages * KB * kLtHalf + 256;
@@ -646,8 +646,8 @@ __global__ void __launch_bounds__(kLtThreads, 1)
       mbar_init(accf + 8 * a, 1);
       mbar_init(acce + 8 * a, 4);
     }
-    mbar_init(hfree, 8);
-    mbar_init(hfull, 8);
+    mbar_init(hfree, kLtEpi / 32);
+    mbar_init(hfull, kLtEpi / 32);
     mbar_init(done_bar, 1);
     fence_mbar_init();
   }
@@ -664,7 +664,9 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   const int num = *p.num_tiles, n = p.n, R = p.R;
   const int nch = (n + 127) >> 7;
   const int64_t units = (int64_t)num * nch;
-  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  const int64_t u0 = units * blockIdx.x / gridDim.x;
+  const int my_units = (int)(units * (blockIdx.x + 1) / gridDim.x - u0);
+  const int t0 = (int)(u0 / nch), ch0 = (int)(u0 - (int64_t)t0 * nch);  // the first unit's tile and columns
   // (units of rows without an adapter are copied by the epilogue warps alone)
 
   if (warp == 0) {
@@ -673,9 +675,10 @@ __global__ void __launch_bounds__(kLtThreads, 1)
       prefetch_tmap(&tm_b);
       uint32_t c = 0, issued = 0;  // stages filled
       const bool withhold = (g_test_flags & kTestWithholdXTiles) != 0;  // test switch: issue nothing
-      for (int64_t u = u0; u < u1 && !withhold; u++) {
-        const int t = (int)(u / nch), ch = (int)(u - (int64_t)t * nch);
-        const RowTile tile = p.tiles[t];
+      RowTile tile = {};
+      for (int u = 0, t = t0, ch = ch0; u < my_units && !withhold; u++, ch++) {
+        if (ch == nch) { ch = 0; t++; }
+        if (u == 0 || ch == 0) tile = p.tiles[t];
         if (tile.g >= p.L || tile.count <= 0) continue;
         const uint32_t s = c % kLtStages;
         if (!gg_wait(empty + 8 * s, ((c / kLtStages) & 1u) ^ 1u)) { s_abort = 1; break; }
@@ -694,25 +697,27 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     // ---------------------------- MMA issuer ------------------------------
     const bool leader = elect_one();
     uint32_t c = 0, tiles = 0;
-    int told = -1, rank = 0;
-    for (int64_t u = u0; u < u1; u++) {
-      const int t = (int)(u / nch);
-      const RowTile tile = p.tiles[t];
+    int k16 = 0;
+    RowTile tile = {};
+    const uint32_t idesc = umma_idesc_f16(128);
+    for (int u = 0, t = t0, ch = ch0; u < my_units; u++, ch++) {
+      if (ch == nch) { ch = 0; t++; }
+      const bool fresh = u == 0 || ch == 0;  // a new tile
+      if (fresh) tile = p.tiles[t];
       if (tile.g >= p.L || tile.count <= 0) continue;
       bool ok = true;
-      if (t != told) {
-        rank = (int)warp_uniform((uint32_t)lora_rank(p, tile.g));
+      if (fresh) {
+        const int rank = (int)warp_uniform((uint32_t)lora_rank(p, tile.g));
+        k16 = max((rank + 15) >> 4, 1);  // (rank 0: one step of zeros)
         ok = gg_wait(hfull, tiles++ & 1u);
-        told = t;
       }
       const uint32_t s = c % kLtStages, a = c & 3u;
-      ok = ok && gg_wait(acce + 8 * a, ((c >> 2) & 1u) ^ 1u) && gg_wait(full + 8 * s, (c / kLtStages) & 1u);
-      if (lora_partial(rank)) ok = ok && gg_wait(fixd + 8 * s, (c / kLtStages) & 1u);
+      // (both barriers for every stage: neither may get a phase ahead of its other waiter)
+      ok = ok && gg_wait(acce + 8 * a, ((c >> 2) & 1u) ^ 1u) && gg_wait(full + 8 * s, (c / kLtStages) & 1u) &&
+           gg_wait(fixd + 8 * s, (c / kLtStages) & 1u);
       if (!__all_sync(0xFFFFFFFFu, ok)) { s_abort = 1; break; }
       tc_fence_after();
-      const uint32_t idesc = umma_idesc_f16(128);
       const uint32_t d = warp_uniform(tmem) + 128u * a;
-      const int k16 = max((rank + 15) >> 4, 1);  // (rank 0: one step of zeros)
       if (leader) {
         for (int kk = 0; kk < k16; kk++) {
           const uint32_t blk = (uint32_t)(kk >> 2) * kLtHalf;
@@ -731,12 +736,16 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   } else if (warp < 4) {
     // ----------------------- ranks inside a k16 step ------------------------
     uint32_t c = 0;
-    for (int64_t u = u0; u < u1; u++) {
-      const RowTile tile = p.tiles[u / nch];
+    int rank = 0;
+    RowTile tile = {};
+    for (int u = 0, t = t0, ch = ch0; u < my_units; u++, ch++) {
+      if (ch == nch) { ch = 0; t++; }
+      if (u == 0 || ch == 0) {
+        tile = p.tiles[t];
+        if (tile.g < p.L) rank = lora_rank(p, tile.g);
+      }
       if (tile.g >= p.L || tile.count <= 0) continue;
-      const int rank = lora_rank(p, tile.g);
       const uint32_t s = c % kLtStages;
-      // (waits for every stage, needed or not: the barrier's phases keep pace)
       const bool ok = gg_wait(full + 8 * s, (c / kLtStages) & 1u);
       if (!__all_sync(0xFFFFFFFFu, ok)) { s_abort = 1; break; }
       if (lora_partial(rank)) {
@@ -761,33 +770,34 @@ __global__ void __launch_bounds__(kLtThreads, 1)
                       ((reinterpret_cast<uintptr_t>(p.base) | reinterpret_cast<uintptr_t>(p.y)) & 31) == 0;
     const int row = 32 * q + lane;  // of the tile: a TMEM lane
     uint32_t c = 0, tiles = 0;
-    int told = -1, tb = 0;
+    int tb = 0;
+    RowTile tile = {};
     float scale = 0.f;
     bool ok = true;
-    for (int64_t u = u0; u < u1 && ok; u++) {
-      const int t = (int)(u / nch), ch = (int)(u - (int64_t)t * nch);
-      const RowTile tile = p.tiles[t];
+    for (int u = 0, t = t0, ch = ch0; u < my_units && ok; u++, ch++) {
+      if (ch == nch) { ch = 0; t++; }
+      const bool fresh = u == 0 || ch == 0;  // a new tile
+      if (fresh) tile = p.tiles[t];
       if (tile.count <= 0) continue;
       if (tile.g >= p.L) {  // rows without an adapter
         const int c0 = ch * 128, c1 = min(c0 + 128, n);
-        for (int i = ew; i < tile.count; i += 8) {
+        for (int i = ew; i < tile.count; i += kLtEpi / 32) {
           const int64_t at = (int64_t)p.perm[tile.start + i] * n;
           copy_span(p.y + at, p.base + at, c0, c1, vec, lane, 32);
         }
         continue;
       }
-      if (t != told) {
-        // a new tile: once every epilogue warp is here, all units of the last one
+      if (fresh) {
+        // once every epilogue warp is here, all units of the last one
         // have been multiplied (each has waited for that tile's last unit)
         warp_arrive(hfree, lane);
         ok = gg_wait(hfree, tiles & 1u);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) { s_abort = 1; break; }
-        told = t;
         tb ^= 1;
         scale = p.scales[tile.g];
         for (int i = tid - 128; i < tile.count; i += kLtEpi) yoff[tb][i] = (int64_t)p.perm[tile.start + i] * n;
-        for (int i0 = ew * 4; i0 < 128; i0 += 32) {
+        for (int i0 = ew * 4; i0 < 128; i0 += kLtEpi / 8) {
           float v[4][2 * KB];
 #pragma unroll
           for (int r = 0; r < 4; r++)
@@ -819,32 +829,35 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) { s_abort = 1; break; }
       }
-      if ((int)(c & 1u) == grp) {
+      if ((int)(c % kLtGroups) == grp) {
         const uint32_t a = c & 3u;
         const int c0 = ch * 128, left = n - c0;  // columns from here on
         const bool live = row < tile.count;
         const uint16_t* bp = p.base + yoff[tb][live ? row : 0] + c0;
         uint16_t* yp = p.y + yoff[tb][live ? row : 0] + c0;
         const float f = factor[tb][row];
-        // base, loaded before the products are waited for
-        uint32_t bv[4][16];
-#pragma unroll
-        for (int j = 0; j < 4; j++)
+        // base, 64 columns ahead of its use (the first before the products are
+        // waited for)
+        uint32_t bv[2][16];
+        auto load_base = [&](int j, uint32_t(&to)[16]) {
 #pragma unroll
           for (int i = 0; i < 2; i++) {
-            uint32_t(&w)[8] = *reinterpret_cast<uint32_t(*)[8]>(&bv[j][8 * i]);
-            const int c = 32 * j + 16 * i;
-            if (live && wide && c < left) {
-              ld256(w, bp + c);
-            } else if (live && vec && c < left) {
-              const uint4 v0 = *reinterpret_cast<const uint4*>(bp + c);
-              const uint4 v1 = c + 8 < left ? *reinterpret_cast<const uint4*>(bp + c + 8) : make_uint4(0u, 0u, 0u, 0u);
+            uint32_t(&w)[8] = *reinterpret_cast<uint32_t(*)[8]>(&to[8 * i]);
+            const int col = 32 * j + 16 * i;
+            if (live && wide && col < left) {
+              ld256(w, bp + col);
+            } else if (live && vec && col < left) {
+              const uint4 v0 = *reinterpret_cast<const uint4*>(bp + col);
+              const uint4 v1 = col + 8 < left ? *reinterpret_cast<const uint4*>(bp + col + 8) : make_uint4(0u, 0u, 0u, 0u);
               w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w; w[4] = v1.x; w[5] = v1.y; w[6] = v1.z; w[7] = v1.w;
             } else {
 #pragma unroll
               for (int x = 0; x < 8; x++) w[x] = 0u;
             }
           }
+        };
+        load_base(0, bv[0]);
+        load_base(1, bv[1]);
         ok = gg_wait(accf + 8 * a, (c >> 2) & 1u);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) { s_abort = 1; break; }
@@ -859,21 +872,22 @@ __global__ void __launch_bounds__(kLtThreads, 1)
             if (vec) {
 #pragma unroll
               for (int i = 0; i < 2; i++) {
-                const int c = 32 * j + 16 * i;
+                const int col = 32 * j + 16 * i;
                 uint32_t o[8];
 #pragma unroll
                 for (int x = 0; x < 8; x++) {
-                  const float2 b = f16x2_to_f32x2(bv[j][8 * i + x]);
+                  const float2 b = f16x2_to_f32x2(bv[j & 1][8 * i + x]);
                   o[x] = f32x2_to_f16x2(fmaf(__uint_as_float(r[16 * i + 2 * x]), f, b.x),
                                         fmaf(__uint_as_float(r[16 * i + 2 * x + 1]), f, b.y));
                 }
                 if (wide) {
-                  if (c < left) st256(yp + c, o);
+                  if (col < left) st256(yp + col, o);
                 } else {
-                  if (c < left) *reinterpret_cast<uint4*>(yp + c) = make_uint4(o[0], o[1], o[2], o[3]);
-                  if (c + 8 < left) *reinterpret_cast<uint4*>(yp + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                  if (col < left) *reinterpret_cast<uint4*>(yp + col) = make_uint4(o[0], o[1], o[2], o[3]);
+                  if (col + 8 < left) *reinterpret_cast<uint4*>(yp + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
               }
+              if (j + 2 < 4) load_base(j + 2, bv[j & 1]);
             } else {
 #pragma unroll
               for (int x = 0; x < 32; x++)
@@ -885,7 +899,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         }
         tc_fence_before();
         warp_arrive(acce + 8 * a, lane);
-      } else if (u + 1 == u1 || (u + 1) / nch != t) {
+      } else if (u + 1 == my_units || ch + 1 == nch) {
         // the tile's last unit is the other group's: wait for its products too,
         // so that h may be written again
         ok = gg_wait(accf + 8 * (c & 3u), (c >> 2) & 1u);

@@ -1612,9 +1612,12 @@ static bool lora_by_row(const qmm_adapters* ad, int64_t m) {
 }
 
 // Rows per tile: A and B are read once per tile, so long inputs take larger
-// ones, short ones smaller, for the number of CTAs.  From 512 rows of rank up
-// to 128 the expanding product runs on tcgen05 (lora_expand_tc_kernel).
-static bool lora_tc(int64_t m, int64_t rank) { return m >= 512 && rank <= 128; }
+// ones, short ones smaller, for the number of CTAs.  From 512 rows the
+// expanding product of ranks above 32, up to 128, runs on tcgen05
+// (lora_expand_tc_kernel); legacy MMAs / tcgen05 on B200, us, 18,560 columns:
+// 2,048 rows of rank 16 40 / 46, rank 64 52 / 48, rank 128 89 / 52; 1,024 rows
+// of rank 64 31 / 29; 512 rows 20.6 / 20.5.
+static bool lora_tc(int64_t m, int64_t rank) { return m >= 512 && rank > 32 && rank <= 128; }
 static int lora_tile_rows(int64_t m, int64_t rank) { return lora_tc(m, rank) ? 128 : m >= 512 ? 64 : 32; }
 static int64_t lora_max_tiles(int64_t L, int64_t m, int64_t rank) {
   return m / lora_tile_rows(m, rank) + std::min(m, L + 1);
