@@ -347,7 +347,8 @@ qmm_status qmm_moe_routed(const qmm_weights* gate, const qmm_weights* up, const 
  * qmm_unpermute: the (token, slot) pairs are sorted by expert, every expert's
  * rows lie together, and each expert's packed weights are decoded once for
  * all of its rows ("Mark-Experimental-V3-8B", section "Mixture-of-Experts
- * (MoE)").  For a decode step qmm_moe_routed is the faster call.
+ * (MoE)").  Below about 100 tokens qmm_moe_routed is the faster call (32
+ * experts, top-4: 64 tokens 95 against 117 us, 256 tokens 208 against 137).
  * ------------------------------------------------------------------------- */
 
 /* qmm_route with the inverse of its permutation: a stable counting sort of
@@ -495,6 +496,8 @@ qmm_status qmm_sync_check(void* stream);
  *   QMM_DEBUG_WAIT_LIMIT_NS     value = the limit in ns (1e3 .. 1e10;
  *                               2e9 by default)
  *   QMM_DEBUG_WITHHOLD_X_TILES  value = 1: the GEMMs' activation loader
+ *                               (and that of the grouped products, and the
+ *                               adapters' tensor-core product's loader of B)
  *                               issues no tile load, so their waits run out
  *                               (nothing is written to y); 0: normal
  *   QMM_DEBUG_WITHHOLD_TILE_COPIES  value = 1: the routed-expert tile kernel

@@ -11,6 +11,11 @@
 // reads 64 KB, writes 48 KB and looks 4,096 pairs up per 64-wide k step, about
 // 1,100 cycles of the 128-byte port for 512 cycles of MMA; with the weights
 // in TMEM the port carries X once in and once out and the lookups, ~650.
+// On B200, 32 IQ4_NL experts over 8,192 rows: gate and up (896 x 2560 each)
+// 114 us, 660 TFLOP/s; down (2560 x 896) 66 us.  What bounds it: the decode's
+// latency (434 ns per step at 16 rows, 262 with the lookups left out, 208 with
+// copies and X left out too; the MMAs of 256 rows are 260), and 5 rounds of
+// tiles where 4.5 would do.
 //
 // Roles per CTA (persistent, one per SM, 24 warps):
 //   warp 0       X rows by TMA (64-row boxes, 128-byte swizzle), kGgStages deep
@@ -202,8 +207,9 @@ __device__ __forceinline__ void gg_decode(uint32_t src, int row, bool valid, uin
 
 // SiLU(z) = z / (1 + e^-z) by the fast exponential and division: off by
 // 2 + 1.2 |z| and 2 fp32 steps, far below half an fp16 step of the result it
-// is rounded to.  (expf and the IEEE division, one warp per scheduler, took
-// longer than the tile's products: gate and up of 8,192 pairs 168 us.)
+// is rounded to.  (With the copies and the decode left out, gate and up of
+// 8,192 pairs took 147 us with expf and the IEEE division, one epilogue warp
+// per scheduler, and 78 us with these.)
 __device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
 
 // Store 32 rows of a warp's columns.  p[i] holds two columns of one row, its

@@ -246,7 +246,7 @@ __global__ void __cluster_dims__(kLoraCluster, 1, 1) __launch_bounds__(kLoraThre
 // so that a lane's 16 bytes of a row are its fragment words.  Partial sums
 // meet in shared memory, then across the cluster, each in a fixed order.
 // (With A read from global memory by every warp the loads of 8 rows' lines per
-// instruction took 38 us for 2,048 rows of rank 128 and k = 4096.)
+// instruction took 38 us for 2,048 rows of rank 128 and k = 4096, so 26.)
 // ---------------------------------------------------------------------------
 constexpr int kShrinkK = 256;                       // k per block
 constexpr int kShrinkRow = kShrinkK * 2 + 64;       // bytes between rows of A in a buffer
@@ -577,11 +577,12 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
 // B, brought by TMA into 128-byte-swizzled stages) are N, and K runs over the
 // rank twice, for the two halves of h, against the same stage of B.  A lane of
 // the epilogue then holds a row's neighbouring columns, 32 bytes a load and
-// store (with the columns as M it held a column, and the exchange between lanes
-// alone was 3/4 of 75 us).  The legacy MMAs of lora_expand_kernel take 34 us of tensor time
-// alone at 2,048 rows of rank 128 and 18,560 columns and their fragments as
-// much again; here the products take 9 us and the stream of base and y is what
-// remains.
+// store (with the columns as M it held a column, and the lanes had to exchange:
+// 75 us against 49 for 2,048 rows of rank 64 and 18,560 columns).  The legacy
+// MMAs of lora_expand_kernel take 34 us of tensor time alone at rank 128 and
+// their fragments as much again (89 us in all); here the products take 9 us (52
+// in all, 37 of them the hand-overs between the roles: what is left when base
+// and y are neither loaded nor stored).
 //
 // Roles (one CTA per SM, an equal run of (tile, 128 columns) units each):
 //   warp 0       B by TMA, kLtStages deep

@@ -21,7 +21,7 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 __device__ unsigned long long g_wait_limit_ns = kWaitLimitNs;
 
 // Test switches (qmm_debug_set), 0 in normal use.  kTestWithholdXTiles: the
-// tensor-core GEMMs' activation loader issues no tile load, so the MMA
+// tensor-core GEMMs' tile loader issues no tile load, so the MMA
 // issuer's wait for the first stage runs out and the kernel takes its
 // timeout path (raise the error word, drain, free tensor memory, return).
 // (The routed-expert tile kernel's switch, which withholds its bulk copies,
