@@ -83,8 +83,9 @@ def test_lora(m, n, k, R, L, how, ranks):
 @pytest.mark.parametrize("m", [1, 9, 100, 300, 700])
 def test_bad_ids_and_ranks_are_reported(m):
     rng = np.random.default_rng(m)
-    A, B, sc, _ = _pool(rng, 3, 16, 72, 64)
-    rk = np.array([16, 99, -3], np.int32)
+    R = 48 if m >= 512 else 16                  # (on the tensor-core product from 512 rows)
+    A, B, sc, _ = _pool(rng, 3, R, 72, 64)
+    rk = np.array([R, 99, -3], np.int32)        # clamped: all of it, all of it, none
     x, base = rng.standard_normal((m, 64)).astype(np.float16), rng.standard_normal((m, 72)).astype(np.float16)
     ids = np.array([[3, -2, 0][i % 3] for i in range(m)], np.int32)
     ad = _adapters(A, B, sc, None)
@@ -102,7 +103,7 @@ def test_values_outside_fp16_between_the_products(m):
     """A x beyond fp16's range and below its smallest step, brought back by B
     and the scale: the middle product is held in fp32."""
     rng = np.random.default_rng(3)
-    L, R, n, k = 2, 16, 64, 512
+    L, R, n, k = 2, 48 if m >= 512 else 16, 64, 512
     A = np.ones((L, R, k), np.float16) * np.float16(400.0)
     A[1] = np.float16(2.0 ** -20)
     x = np.abs(rng.standard_normal((m, k)) + 2).astype(np.float16)
@@ -118,7 +119,7 @@ def test_values_outside_fp16_between_the_products(m):
 @pytest.mark.parametrize("m", [2, 40, 300, 700])
 def test_infinities_and_nan_stay_in_their_row(m):
     rng = np.random.default_rng(4)
-    A, B, sc, _ = _pool(rng, 2, 32, 136, 256)
+    A, B, sc, _ = _pool(rng, 2, 48 if m >= 512 else 32, 136, 256)
     x, base = rng.standard_normal((m, 256)).astype(np.float16), rng.standard_normal((m, 136)).astype(np.float16)
     ids = (np.arange(m) % 2).astype(np.int32)
     x[0, 5] = np.nan
@@ -135,7 +136,7 @@ def test_an_infinite_middle_product_gives_what_fp32_gives():
     """An infinity in x: A x is +-inf, and the outputs are +-inf or NaN where
     infinities of both signs (or 0 * inf) meet."""
     for m in (1, 70, 600):
-        L, R, n, k = 1, 8, 16, 64
+        L, R, n, k = 1, 40 if m >= 512 else 8, 16, 64
         A, B = np.ones((L, R, k), np.float16), np.ones((L, n, R), np.float16)
         B[0, 1] = -1
         B[0, 2, :4] = -1
@@ -148,18 +149,45 @@ def test_an_infinite_middle_product_gives_what_fp32_gives():
         assert np.isfinite(y[1:]).all()
 
 
-def test_strided_pool():
-    """Adapters further apart than their size."""
+@pytest.mark.parametrize("m,R", [(3, 16), (70, 16), (600, 16), (600, 72)])
+def test_strided_pool_and_shifted_buffers(m, R):
+    """Adapters further apart than their size; base and y 16 bytes into an
+    allocation (aligned to 16, not to 32)."""
     rng = np.random.default_rng(6)
-    A, B, sc, _ = _pool(rng, 4, 16, 72, 64)
-    big_a, big_b = np.full((4, 24, 64), np.nan, np.float16), np.full((4, 80, 16), np.nan, np.float16)
-    big_a[:, :16], big_b[:, :72] = A, B
-    ad = qmm.Adapters(torch.from_numpy(big_a).cuda()[:, :16], torch.from_numpy(big_b).cuda()[:, :72],
+    n = 80
+    A, B, sc, _ = _pool(rng, 4, R, n, 64)
+    big_a, big_b = np.full((4, R + 8, 64), np.nan, np.float16), np.full((4, n + 8, R), np.nan, np.float16)
+    big_a[:, :R], big_b[:, :n] = A, B
+    ad = qmm.Adapters(torch.from_numpy(big_a).cuda()[:, :R], torch.from_numpy(big_b).cuda()[:, :n],
                       torch.from_numpy(sc).cuda())
-    for m in (3, 70, 600):
-        x, base = rng.standard_normal((m, 64)).astype(np.float16), rng.standard_normal((m, 72)).astype(np.float16)
-        ids = _ids(rng, m, 4, "any")
-        within(_run(ad, x, ids, base).cpu().numpy(), *lora(_d(x), _d(base), ids, _d(A), _d(B), sc, None))
+    x, base = rng.standard_normal((m, 64)).astype(np.float16), rng.standard_normal((m, n)).astype(np.float16)
+    ids = _ids(rng, m, 4, "any")
+    ref, bound = lora(_d(x), _d(base), ids, _d(A), _d(B), sc, None)
+    y = _run(ad, x, ids, base)
+    within(y.cpu().numpy(), ref, bound)
+    buf = torch.full((m * n + 24,), 7.0, dtype=torch.float16, device="cuda")
+    shifted = buf[8:8 + m * n].view(m, n)
+    shifted.copy_(torch.from_numpy(base))
+    ws = torch.empty(qmm.qmm_lora_workspace_bytes(ad, m), dtype=torch.uint8, device="cuda")
+    qmm.qmm_lora(ad, torch.from_numpy(x).cuda(), torch.from_numpy(ids).cuda(), shifted, shifted, ws=ws)
+    assert torch.equal(shifted, y)
+    assert bool((buf[:8] == 7).all()) and bool((buf[8 + m * n:] == 7).all())
+
+
+@pytest.mark.parametrize("m", [40, 600])
+def test_every_rank_of_a_pool(m):
+    """Ranks 0 .. R one adapter each, what they leave out not a number."""
+    rng = np.random.default_rng(m)
+    R, n, k = 64, 136, 72
+    A, B, sc, _ = _pool(rng, R + 1, R, n, k)
+    rk = np.arange(R + 1, dtype=np.int32)
+    for a in range(R + 1):
+        A[a, a:], B[a][:, a:] = np.nan, np.nan
+    x, base = rng.standard_normal((m, k)).astype(np.float16), rng.standard_normal((m, n)).astype(np.float16)
+    ids = (np.arange(m) % (R + 1)).astype(np.int32)
+    y = _run(_adapters(A, B, sc, rk), x, ids, base)
+    assert qmm.qmm_sync_check() == 0
+    within(y.cpu().numpy(), *lora(_d(x), _d(base), ids, _d(A), _d(B), sc, rk), qmm.qmm_last_variant())
 
 
 def test_zero_sizes():

@@ -51,6 +51,24 @@ def test_route_rows_reports_ids_out_of_range():
     assert off.cpu().tolist() == [0, 1, 3, 3, 4, 4, 4, 4, 4]
 
 
+def test_no_pairs():
+    """No tokens, and tokens without slots: the offsets are zeros, an output
+    row without slots is zero."""
+    off = torch.full((6,), -7, dtype=torch.int32, device="cuda")
+    for t, topk in ((0, 4), (3, 0)):
+        e = torch.empty((t, topk), dtype=torch.int32, device="cuda")
+        qmm.qmm_route_rows(e, 5, off, e, e)
+        assert off.tolist() == [0] * 6
+        x = torch.ones((t, 16), dtype=torch.float16, device="cuda")
+        xs = torch.empty((0, 16), dtype=torch.float16, device="cuda")
+        qmm.qmm_permute(x, e, xs)
+        out = torch.full_like(x, 7.0)
+        qmm.qmm_unpermute(xs, e, None, out)
+        assert bool((out == 0).all())
+        qmm.qmm_unpermute_backward(x, xs, e, None, xs, torch.empty((t, topk), device="cuda"))
+    assert qmm.qmm_sync_check() == 0
+
+
 SHAPES = [(1, 1, 4, 8, 0), (4, 4, 32, 2560, 0), (17, 6, 64, 896, 3), (33, 3, 8, 1032, 0), (300, 2, 13, 4096, 300),
           (515, 8, 128, 264, 50), (2100, 4, 32, 2560, 0)]
 
