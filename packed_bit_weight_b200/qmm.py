@@ -389,16 +389,30 @@ def qmm_moe_routed(gate: PackedWeights, up: PackedWeights, down: PackedWeights, 
 
 
 # -- rows grouped by expert ------------------------------------------------------
-def _here(t: torch.Tensor | None, esize: int | None, name: str):
-    """_ptr for a tensor that must be on the current device (the C ABI
-    launches there, whatever device the pointer is of)."""
+def _dev() -> int:
+    """The current device, -1 before CUDA is in use."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+
+
+def _here(t: torch.Tensor | None, esize: int | None, name: str, dev: int):
+    """The address of a tensor that must be on the current device `dev` (the C
+    ABI launches there, whatever device the pointer is of)."""
     if t is None:
         return None
-    if not (t.is_cuda and t.is_contiguous() and (esize is None or t.element_size() == esize)):
-        _ptr(t, esize, name)  # says what is wrong
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
-    return t.data_ptr()
+    if t.get_device() == dev >= 0 and t.is_contiguous() and (esize is None or t.element_size() == esize):
+        return t.data_ptr()
+    _ptr(t, esize, name)  # says what is wrong
+    raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, dev))
+
+
+def _weights_here(w: PackedWeights, dev: int) -> None:
+    _here(w.data, None, "data", dev)
+    _here(w.scales, None, "scales", dev)
+
+
+def _stream_on(stream, dev: int):
+    """The raw handle of the stream (a Stream object costs more than a launch)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def qmm_route_rows(topk_ids: torch.Tensor, num_experts: int, offsets: torch.Tensor, perm: torch.Tensor,
@@ -409,8 +423,10 @@ def qmm_route_rows(topk_ids: torch.Tensor, num_experts: int, offsets: torch.Tens
     _need(offsets, 4 * (num_experts + 1), "offsets")
     _need(perm, 4 * t * topk, "perm")
     _need(rows, 4 * t * topk, "rows")
-    _check(_lib().qmm_route_rows(_here(topk_ids, 4, "topk_ids"), t, topk, num_experts, _here(offsets, 4, "offsets"),
-                                 _here(perm, 4, "perm"), _here(rows, 4, "rows"), _stream(stream)), "qmm_route_rows")
+    dev = _dev()
+    _check(_lib().qmm_route_rows(_here(topk_ids, 4, "topk_ids", dev), t, topk, num_experts,
+                                 _here(offsets, 4, "offsets", dev), _here(perm, 4, "perm", dev),
+                                 _here(rows, 4, "rows", dev), _stream_on(stream, dev)), "qmm_route_rows")
     return offsets, perm, rows
 
 
@@ -431,16 +447,18 @@ def _need_rows(rows: torch.Tensor, tok: torch.Tensor, tok_name: str, sorted_rows
 def qmm_permute(x: torch.Tensor, rows: torch.Tensor, xs: torch.Tensor, stream=None) -> torch.Tensor:
     """xs[rows[t][s]] = x[t]: x [t][d] -> xs [t*topk][d]."""
     t, topk, d = _need_rows(rows, x, "x", ((xs, "xs"),))
-    _check(_lib().qmm_permute(_here(x, 2, "x"), _here(rows, 4, "rows"), t, topk, d, _here(xs, 2, "xs"),
-                              _stream(stream)), "qmm_permute")
+    dev = _dev()
+    _check(_lib().qmm_permute(_here(x, 2, "x", dev), _here(rows, 4, "rows", dev), t, topk, d, _here(xs, 2, "xs", dev),
+                              _stream_on(stream, dev)), "qmm_permute")
     return xs
 
 
 def qmm_permute_backward(dxs: torch.Tensor, rows: torch.Tensor, dx: torch.Tensor, stream=None) -> torch.Tensor:
     """dx[t] = sum_s dxs[rows[t][s]]: the gradient of qmm_permute."""
     t, topk, d = _need_rows(rows, dx, "dx", ((dxs, "dxs"),))
-    _check(_lib().qmm_permute_backward(_here(dxs, 2, "dxs"), _here(rows, 4, "rows"), t, topk, d, _here(dx, 2, "dx"),
-                                       _stream(stream)), "qmm_permute_backward")
+    dev = _dev()
+    _check(_lib().qmm_permute_backward(_here(dxs, 2, "dxs", dev), _here(rows, 4, "rows", dev), t, topk, d,
+                                       _here(dx, 2, "dx", dev), _stream_on(stream, dev)), "qmm_permute_backward")
     return dx
 
 
@@ -449,8 +467,10 @@ def qmm_unpermute(ys: torch.Tensor, rows: torch.Tensor, topk_weights: torch.Tens
     """out[t] = sum_s topk_weights[t][s] * ys[rows[t][s]] (weights of 1 when
     None): ys [t*topk][d] -> out [t][d]."""
     t, topk, d = _need_rows(rows, out, "out", ((ys, "ys"),), ((topk_weights, "topk_weights"),))
-    _check(_lib().qmm_unpermute(_here(ys, 2, "ys"), _here(rows, 4, "rows"), _here(topk_weights, 4, "topk_weights"),
-                                t, topk, d, _here(out, 2, "out"), _stream(stream)), "qmm_unpermute")
+    dev = _dev()
+    _check(_lib().qmm_unpermute(_here(ys, 2, "ys", dev), _here(rows, 4, "rows", dev),
+                                _here(topk_weights, 4, "topk_weights", dev), t, topk, d, _here(out, 2, "out", dev),
+                                _stream_on(stream, dev)), "qmm_unpermute")
     return out
 
 
@@ -460,9 +480,11 @@ def qmm_unpermute_backward(dout: torch.Tensor, ys: torch.Tensor, rows: torch.Ten
     """The gradients of qmm_unpermute: dys [t*topk][d] and dweights [t][topk]."""
     t, topk, d = _need_rows(rows, dout, "dout", ((ys, "ys"), (dys, "dys")),
                             ((topk_weights, "topk_weights"), (dweights, "dweights")))
-    _check(_lib().qmm_unpermute_backward(_here(dout, 2, "dout"), _here(ys, 2, "ys"), _here(rows, 4, "rows"),
-                                         _here(topk_weights, 4, "topk_weights"), t, topk, d, _here(dys, 2, "dys"),
-                                         _here(dweights, 4, "dweights"), _stream(stream)), "qmm_unpermute_backward")
+    dev = _dev()
+    _check(_lib().qmm_unpermute_backward(_here(dout, 2, "dout", dev), _here(ys, 2, "ys", dev),
+                                         _here(rows, 4, "rows", dev), _here(topk_weights, 4, "topk_weights", dev),
+                                         t, topk, d, _here(dys, 2, "dys", dev), _here(dweights, 4, "dweights", dev),
+                                         _stream_on(stream, dev)), "qmm_unpermute_backward")
     return dys, dweights
 
 
@@ -473,8 +495,10 @@ def qmm_grouped_gemm(w: PackedWeights, xs: torch.Tensor, offsets: torch.Tensor, 
     _need(xs, 2 * xs.shape[0] * w.k, "xs")
     _need(ys, 2 * xs.shape[0] * w.n, "ys")
     _need(offsets, 4 * (w.experts + 1), "offsets")
-    _check(_lib().qmm_grouped_gemm(ctypes.byref(d), _here(xs, 2, "xs"), _here(offsets, 4, "offsets"), xs.shape[0],
-                                   _here(ys, 2, "ys"), _stream(stream)), "qmm_grouped_gemm")
+    dev = _dev()
+    _weights_here(w, dev)
+    _check(_lib().qmm_grouped_gemm(ctypes.byref(d), _here(xs, 2, "xs", dev), _here(offsets, 4, "offsets", dev),
+                                   xs.shape[0], _here(ys, 2, "ys", dev), _stream_on(stream, dev)), "qmm_grouped_gemm")
     return ys
 
 
@@ -485,9 +509,12 @@ def qmm_grouped_swiglu(gate: PackedWeights, up: PackedWeights, xs: torch.Tensor,
     _need(xs, 2 * xs.shape[0] * gate.k, "xs")
     _need(h, 2 * xs.shape[0] * gate.n, "h")
     _need(offsets, 4 * (gate.experts + 1), "offsets")
-    _check(_lib().qmm_grouped_swiglu(ctypes.byref(dg), ctypes.byref(du), _here(xs, 2, "xs"),
-                                     _here(offsets, 4, "offsets"), xs.shape[0], _here(h, 2, "h"),
-                                     _stream(stream)), "qmm_grouped_swiglu")
+    dev = _dev()
+    _weights_here(gate, dev)
+    _weights_here(up, dev)
+    _check(_lib().qmm_grouped_swiglu(ctypes.byref(dg), ctypes.byref(du), _here(xs, 2, "xs", dev),
+                                     _here(offsets, 4, "offsets", dev), xs.shape[0], _here(h, 2, "h", dev),
+                                     _stream_on(stream, dev)), "qmm_grouped_swiglu")
     return h
 
 
@@ -503,16 +530,21 @@ class Adapters:
     ranks: torch.Tensor | None = None
 
     def desc(self) -> qmm_adapters:
-        """The C descriptor, rebuilt only when a tensor was replaced or moved."""
-        key = tuple(None if t is None else (t.data_ptr(), t.shape, t.stride(), t.device)
-                    for t in (self.a, self.b, self.scales, self.ranks)) + (torch.cuda.current_device()
-                                                                           if self.a.is_cuda else None,)
+        """The C descriptor, rebuilt only when a tensor was replaced or moved
+        or another device became current."""
+        a, b, s, r = self.a, self.b, self.scales, self.ranks
+        key = (a.data_ptr(), b.data_ptr(), s.data_ptr(), 0 if r is None else r.data_ptr(), a.shape, b.shape,
+               a.stride(), b.stride(), s.numel(), a.get_device(), _dev())
         cached = self.__dict__.get("_desc")
         if cached is not None and cached[0] == key:
             return cached[1]
         d = self._build_desc()
-        self.__dict__["_desc"] = (key, d)
+        self.__dict__["_desc"] = (key, d, ctypes.byref(d))
         return d
+
+    def _ref(self):
+        self.desc()
+        return self.__dict__["_desc"][2]
 
     def _build_desc(self) -> qmm_adapters:
         a, b = self.a, self.b
@@ -532,18 +564,17 @@ class Adapters:
                 raise ValueError("%s must be a CUDA tensor" % name)
             if t.element_size() != 2:
                 raise ValueError("%s must have 2-byte elements" % name)
-            if t.device.index != torch.cuda.current_device():
-                raise ValueError("%s is on %s, the current device is cuda:%d" %
-                                 (name, t.device, torch.cuda.current_device()))
+            if t.get_device() != _dev():
+                raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, _dev()))
         d.a, d.b = ctypes.c_void_p(a.data_ptr()), ctypes.c_void_p(b.data_ptr())
         d.a_stride = 2 * (a.stride(0) if L > 1 else R * k)
         d.b_stride = 2 * (b.stride(0) if L > 1 else n * R)
-        d.scales, d.ranks = _here(self.scales, 4, "scales"), _here(self.ranks, 4, "ranks")
+        d.scales, d.ranks = _here(self.scales, 4, "scales", _dev()), _here(self.ranks, 4, "ranks", _dev())
         return d
 
 
 def qmm_lora_workspace_bytes(adapters: Adapters, m: int) -> int:
-    return _lib().qmm_lora_workspace_bytes(ctypes.byref(adapters.desc()), m)
+    return _lib().qmm_lora_workspace_bytes(adapters._ref(), m)
 
 
 def qmm_lora(adapters: Adapters, x: torch.Tensor, adapter_ids: torch.Tensor, base: torch.Tensor, y: torch.Tensor,
@@ -554,12 +585,11 @@ def qmm_lora(adapters: Adapters, x: torch.Tensor, adapter_ids: torch.Tensor, bas
     _need(x, 2 * m * k, "x")
     _need(base, 2 * m * n, "base")
     _need(y, 2 * m * n, "y")
-    d = adapters.desc()
-    wp, wb = _ws(ws)
-    if ws is not None:
-        _here(ws, None, "ws")
-    _check(_lib().qmm_lora(ctypes.byref(d), _here(x, 2, "x"), _here(adapter_ids, 4, "adapter_ids"), m,
-                           _here(base, 2, "base"), _here(y, 2, "y"), wp, wb, _stream(stream)), "qmm_lora")
+    dev = _dev()
+    wb = 0 if ws is None else ws.nbytes
+    _check(_lib().qmm_lora(adapters._ref(), _here(x, 2, "x", dev), _here(adapter_ids, 4, "adapter_ids", dev), m,
+                           _here(base, 2, "base", dev), _here(y, 2, "y", dev), _here(ws, None, "ws", dev), wb,
+                           _stream_on(stream, dev)), "qmm_lora")
     return y
 
 
