@@ -56,7 +56,8 @@ constexpr int kGgCopyWarps = 2, kGgGroups = 4, kGgDecodeWarps = 4 * kGgGroups;
 constexpr int kGgThreads = (2 + kGgCopyWarps + kGgDecodeWarps + 4) * 32;
 constexpr int kGgCodes = kGgRows * 128;           // FP4 slot: codes [128][128 B] (unit u of row r at u ^ (r & 7))
 constexpr int kGgSlotFp4 = kGgCodes + kGgRows * 32;   // then scales [128][32 B]
-constexpr int kGgSlotIq4 = kGgRows * 144;         // IQ4_NL slot: [128 rows][144 B] (9 units: 16-byte reads of 8 rows hit 8 bank groups)
+// IQ4_NL slot: [128 rows][144 B] (9 units: 16-byte reads of 8 rows hit 8 bank groups)
+constexpr int kGgSlotIq4 = kGgRows * 144;
 constexpr uint32_t kGgAccCol = 0, kGgACol = 384;  // TMEM columns: 3 x 128 accumulators, 4 x 32 weights
 
 struct GgArgs {
@@ -441,7 +442,9 @@ __global__ void __launch_bounds__(kGgThreads, 1)
     const int lr = lane / kLanes, u = lane % kLanes;
     // tile row 64 cw + i (i < 64, its low part may depend on the lane) as a
     // weight row; its stack with SWI is (i >> 4) & 1
-    auto wrow = [&](int n0, int i) { return min(SWI ? n0 + 32 * cw + ((i >> 5) << 4) + (i & 15) : n0 + 64 * cw + i, n - 1); };
+    auto wrow = [&](int n0, int i) {
+      return min(SWI ? n0 + 32 * cw + ((i >> 5) << 4) + (i & 15) : n0 + 64 * cw + i, n - 1);
+    };
     int ck = 0;  // chunks so far
     bool ok = true;
     for (int li = 0; li < my_tiles && ok; li++) {

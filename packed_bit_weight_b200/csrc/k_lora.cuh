@@ -417,157 +417,158 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
   const int64_t u1 = units * (blockIdx.x + 1) / gridDim.x;
   int run = 0;
   for (int64_t u = units * blockIdx.x / gridDim.x; u < u1; u += run) {
-  const int t = (int)(u / nch), first = (int)(u - (int64_t)t * nch);
-  run = (int)min((int64_t)(nch - first), u1 - u);
-  const RowTile tile = p.tiles[t];
-  const int c0 = first * 256, c1 = min((first + run) * 256, n);
-  if (tile.count <= 0) continue;
-  __syncthreads();  // (the last item's rows and fragments are no longer read)
-  for (int i = tid; i < tile.count; i += kLoraThreads) yoff[i] = (int64_t)p.perm[tile.start + i] * n;
-  if (tile.g >= p.L) {  // rows without an adapter
+    const int t = (int)(u / nch), first = (int)(u - (int64_t)t * nch);
+    run = (int)min((int64_t)(nch - first), u1 - u);
+    const RowTile tile = p.tiles[t];
+    const int c0 = first * 256, c1 = min((first + run) * 256, n);
+    if (tile.count <= 0) continue;
+    __syncthreads();  // (the last item's rows and fragments are no longer read)
+    for (int i = tid; i < tile.count; i += kLoraThreads) yoff[i] = (int64_t)p.perm[tile.start + i] * n;
+    if (tile.g >= p.L) {  // rows without an adapter
+      __syncthreads();
+      for (int i = warp; i < tile.count; i += kLoraWarps) {
+        const int64_t at = yoff[i];
+        copy_span(p.y + at, p.base + at, c0, c1, (n & 7) == 0, lane, 32);
+      }
+      continue;
+    }
+    const int rank = lora_rank(p, tile.g);
+    const float scale = p.scales[tile.g];
+    const int groups = (tile.count + 15) >> 4;
+    // fragments of h: kAtOnce rows per warp at a time
+    constexpr int kAtOnce = KC <= 4 ? 4 : 2;
+    for (int i0 = warp * kAtOnce; i0 < groups * 16; i0 += kLoraWarps * kAtOnce) {
+      float v[kAtOnce][KC];
+#pragma unroll
+      for (int r = 0; r < kAtOnce; r++)
+#pragma unroll
+        for (int c = 0; c < KC; c++)
+          v[r][c] = (i0 + r < tile.count && 32 * c + lane < R) ? p.h[(int64_t)(tile.start + i0 + r) * R + 32 * c + lane]
+                                                               : 0.f;
+#pragma unroll
+      for (int r = 0; r < kAtOnce; r++) {
+        const int i = i0 + r;
+        float f1, f2, back;
+        h_scale<KC>(v[r], f1, f2, back);
+        if (lane == 0) factor[i] = scale * back;
+        // column r = 32 c + 8 t + 4 s + 2 w + b of row i: word (row half) + 2 w of
+        // lane (i % 8, t), step s of chunk c, half b
+        const int t = lane >> 3, s = (lane >> 2) & 1, w = (lane >> 1) & 1, b = lane & 1;
+        const int word = ((i >> 3) & 1) + 2 * w, to = ((i & 7) << 2) | t;
+#pragma unroll
+        for (int c = 0; c < KC; c++) {
+          uint16_t hi, lo;
+          h_split(v[r][c] * f1 * f2, hi, lo);
+          uint16_t* f = reinterpret_cast<uint16_t*>(frag + ((((i >> 4) * KC + c) * 2 + s) * 2) * 32 + to);
+          f[word * 2 + b] = hi;
+          f[32 * 8 + word * 2 + b] = lo;
+        }
+      }
+    }
     __syncthreads();
-    for (int i = warp; i < tile.count; i += kLoraWarps) {
-      const int64_t at = yoff[i];
-      copy_span(p.y + at, p.base + at, c0, c1, (n & 7) == 0, lane, 32);
-    }
-    continue;
-  }
-  const int rank = lora_rank(p, tile.g);
-  const float scale = p.scales[tile.g];
-  const int groups = (tile.count + 15) >> 4;
-  // fragments of h: kAtOnce rows per warp at a time
-  constexpr int kAtOnce = KC <= 4 ? 4 : 2;
-  for (int i0 = warp * kAtOnce; i0 < groups * 16; i0 += kLoraWarps * kAtOnce) {
-    float v[kAtOnce][KC];
+    const uint16_t* B = lora_b(p, tile.g);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const bool vec = (n & 7) == 0;
+    for (int nb = c0 + warp * 32; nb < c1; nb += kLoraWarps * 32) {
+      uint4 w[4][KC];
 #pragma unroll
-    for (int r = 0; r < kAtOnce; r++)
+      for (int j = 0; j < 4; j++) {
+        const int col = nb + 8 * (grp >> 1) + 2 * j + (grp & 1);
 #pragma unroll
-      for (int c = 0; c < KC; c++)
-        v[r][c] = (i0 + r < tile.count && 32 * c + lane < R) ? p.h[(int64_t)(tile.start + i0 + r) * R + 32 * c + lane]
-                                                             : 0.f;
-#pragma unroll
-    for (int r = 0; r < kAtOnce; r++) {
-    const int i = i0 + r;
-    float f1, f2, back;
-    h_scale<KC>(v[r], f1, f2, back);
-    if (lane == 0) factor[i] = scale * back;
-    // column r = 32 c + 8 t + 4 s + 2 w + b of row i: word (row half) + 2 w of lane (i % 8, t), step s of chunk c, half b
-    const int t = lane >> 3, s = (lane >> 2) & 1, w = (lane >> 1) & 1, b = lane & 1;
-    const int word = ((i >> 3) & 1) + 2 * w, to = ((i & 7) << 2) | t;
-#pragma unroll
-    for (int c = 0; c < KC; c++) {
-      uint16_t hi, lo;
-      h_split(v[r][c] * f1 * f2, hi, lo);
-      uint16_t* f = reinterpret_cast<uint16_t*>(frag + ((((i >> 4) * KC + c) * 2 + s) * 2) * 32 + to);
-      f[word * 2 + b] = hi;
-      f[32 * 8 + word * 2 + b] = lo;
-    }
-    }
-  }
-  __syncthreads();
-  const uint16_t* B = lora_b(p, tile.g);
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  const bool vec = (n & 7) == 0;
-  for (int nb = c0 + warp * 32; nb < c1; nb += kLoraWarps * 32) {
-    uint4 w[4][KC];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const int col = nb + 8 * (grp >> 1) + 2 * j + (grp & 1);
-#pragma unroll
-      for (int c = 0; c < KC; c++) {
-        const int r = 32 * c + 8 * tig;
-        w[j][c] = (col < n && r < rank) ? *reinterpret_cast<const uint4*>(B + (int64_t)col * R + r) : zero;
-      }
-    }
-    // the next columns' rows of B on their way into L2 meanwhile
-    const int ncol = nb + kLoraWarps * 32 + lane;
-    if (ncol < c1)
-      for (int r = 0; r < rank; r += 64)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(B + (int64_t)ncol * R + r));
-    const int col = nb + 8 * tig;  // this lane's 8 columns
-    // base, kAhead row groups ahead of its use (loads stay behind the stores
-    // they follow: y may be base)
-    constexpr int kAhead = KC <= 4 ? 3 : 1;
-    uint4 ahead[kAhead][2];
-    auto load_base = [&](int g, uint4 (&v)[2]) {
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const int i = g * 16 + grp + 8 * h;
-        v[h] = (vec && i < tile.count && col < c1)
-                   ? *reinterpret_cast<const uint4*>(p.base + yoff[i] + col)
-                   : zero;
-      }
-    };
-#pragma unroll
-    for (int d = 0; d < kAhead; d++) load_base(d, ahead[d]);
-    if (rank & 7) {  // (after the loads: a use between them would make each wait for the last)
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-#pragma unroll
-        for (int c = 0; c < KC; c++) w[j][c] = mask8(w[j][c], rank - (32 * c + 8 * tig));
-    }
-    for (int g0 = 0; g0 < groups; g0 += kAhead) {
-#pragma unroll
-    for (int d = 0; d < kAhead; d++) {
-      const int g = g0 + d;
-      if (g >= groups) break;
-      const int i0 = g * 16 + grp, i1 = i0 + 8;
-      const bool ok0 = i0 < tile.count, ok1 = i1 < tile.count;
-      const int64_t at0 = yoff[ok0 ? i0 : 0] + col, at1 = yoff[ok1 ? i1 : 0] + col;
-      const uint4 b0 = ahead[d][0], b1 = ahead[d][1];
-      load_base(g + kAhead, ahead[d]);
-      float acc[4][4];
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-#pragma unroll
-        for (int c = 0; c < 4; c++) acc[j][c] = 0.f;
-#pragma unroll
-      for (int c = 0; c < KC; c++) {
-        if (32 * c >= rank) break;
-#pragma unroll
-        for (int s = 0; s < 2; s++) {
-          const uint4* f = frag + (((g * KC + c) * 2 + s) * 2) * 32 + lane;
-          const uint4 hi = f[0], lo = f[32];
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const uint32_t v0 = s ? w[j][c].z : w[j][c].x, v1 = s ? w[j][c].w : w[j][c].y;
-            mma_16816(acc[j], hi.x, hi.y, hi.z, hi.w, v0, v1);
-            mma_16816(acc[j], lo.x, lo.y, lo.z, lo.w, v0, v1);
-          }
+        for (int c = 0; c < KC; c++) {
+          const int r = 32 * c + 8 * tig;
+          w[j][c] = (col < n && r < rank) ? *reinterpret_cast<const uint4*>(B + (int64_t)col * R + r) : zero;
         }
       }
-      // acc[j][0..1]: row i0, columns col + 2j, + 1; acc[j][2..3]: row i1
-      const float q0 = factor[i0], q1 = factor[i1];
-      if (vec) {
-        const uint32_t bw0[4] = {b0.x, b0.y, b0.z, b0.w}, bw1[4] = {b1.x, b1.y, b1.z, b1.w};
-        uint32_t o0[4], o1[4];
+      // the next columns' rows of B on their way into L2 meanwhile
+      const int ncol = nb + kLoraWarps * 32 + lane;
+      if (ncol < c1)
+        for (int r = 0; r < rank; r += 64)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(B + (int64_t)ncol * R + r));
+      const int col = nb + 8 * tig;  // this lane's 8 columns
+      // base, kAhead row groups ahead of its use (loads stay behind the stores
+      // they follow: y may be base)
+      constexpr int kAhead = KC <= 4 ? 3 : 1;
+      uint4 ahead[kAhead][2];
+      auto load_base = [&](int g, uint4 (&v)[2]) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const float2 f0 = f16x2_to_f32x2(bw0[j]), f1 = f16x2_to_f32x2(bw1[j]);
-          o0[j] = f32x2_to_f16x2(fmaf(acc[j][0], q0, f0.x), fmaf(acc[j][1], q0, f0.y));
-          o1[j] = f32x2_to_f16x2(fmaf(acc[j][2], q1, f1.x), fmaf(acc[j][3], q1, f1.y));
+        for (int h = 0; h < 2; h++) {
+          const int i = g * 16 + grp + 8 * h;
+          v[h] = (vec && i < tile.count && col < c1)
+                     ? *reinterpret_cast<const uint4*>(p.base + yoff[i] + col)
+                     : zero;
         }
-        if (ok0 && col < c1) *reinterpret_cast<uint4*>(p.y + at0) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-        if (ok1 && col < c1) *reinterpret_cast<uint4*>(p.y + at1) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-      } else {
+      };
+#pragma unroll
+      for (int d = 0; d < kAhead; d++) load_base(d, ahead[d]);
+      if (rank & 7) {  // (after the loads: a use between them would make each wait for the last)
 #pragma unroll
         for (int j = 0; j < 4; j++)
 #pragma unroll
-          for (int b = 0; b < 2; b++) {
-            if (col + 2 * j + b >= c1) continue;
-            if (ok0) {
-              const int64_t at = at0 + 2 * j + b;
-              p.y[at] = f32_to_f16_bits(fmaf(acc[j][b], q0, __half2float(__ushort_as_half(p.base[at]))));
-            }
-            if (ok1) {
-              const int64_t at = at1 + 2 * j + b;
-              p.y[at] = f32_to_f16_bits(fmaf(acc[j][b + 2], q1, __half2float(__ushort_as_half(p.base[at]))));
+          for (int c = 0; c < KC; c++) w[j][c] = mask8(w[j][c], rank - (32 * c + 8 * tig));
+      }
+      for (int g0 = 0; g0 < groups; g0 += kAhead) {
+#pragma unroll
+        for (int d = 0; d < kAhead; d++) {
+          const int g = g0 + d;
+          if (g >= groups) break;
+          const int i0 = g * 16 + grp, i1 = i0 + 8;
+          const bool ok0 = i0 < tile.count, ok1 = i1 < tile.count;
+          const int64_t at0 = yoff[ok0 ? i0 : 0] + col, at1 = yoff[ok1 ? i1 : 0] + col;
+          const uint4 b0 = ahead[d][0], b1 = ahead[d][1];
+          load_base(g + kAhead, ahead[d]);
+          float acc[4][4];
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) acc[j][c] = 0.f;
+#pragma unroll
+          for (int c = 0; c < KC; c++) {
+            if (32 * c >= rank) break;
+#pragma unroll
+            for (int s = 0; s < 2; s++) {
+              const uint4* f = frag + (((g * KC + c) * 2 + s) * 2) * 32 + lane;
+              const uint4 hi = f[0], lo = f[32];
+#pragma unroll
+              for (int j = 0; j < 4; j++) {
+                const uint32_t v0 = s ? w[j][c].z : w[j][c].x, v1 = s ? w[j][c].w : w[j][c].y;
+                mma_16816(acc[j], hi.x, hi.y, hi.z, hi.w, v0, v1);
+                mma_16816(acc[j], lo.x, lo.y, lo.z, lo.w, v0, v1);
+              }
             }
           }
+          // acc[j][0..1]: row i0, columns col + 2j, + 1; acc[j][2..3]: row i1
+          const float q0 = factor[i0], q1 = factor[i1];
+          if (vec) {
+            const uint32_t bw0[4] = {b0.x, b0.y, b0.z, b0.w}, bw1[4] = {b1.x, b1.y, b1.z, b1.w};
+            uint32_t o0[4], o1[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+              const float2 f0 = f16x2_to_f32x2(bw0[j]), f1 = f16x2_to_f32x2(bw1[j]);
+              o0[j] = f32x2_to_f16x2(fmaf(acc[j][0], q0, f0.x), fmaf(acc[j][1], q0, f0.y));
+              o1[j] = f32x2_to_f16x2(fmaf(acc[j][2], q1, f1.x), fmaf(acc[j][3], q1, f1.y));
+            }
+            if (ok0 && col < c1) *reinterpret_cast<uint4*>(p.y + at0) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+            if (ok1 && col < c1) *reinterpret_cast<uint4*>(p.y + at1) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+              for (int b = 0; b < 2; b++) {
+              if (col + 2 * j + b >= c1) continue;
+              if (ok0) {
+                const int64_t at = at0 + 2 * j + b;
+                p.y[at] = f32_to_f16_bits(fmaf(acc[j][b], q0, __half2float(__ushort_as_half(p.base[at]))));
+              }
+              if (ok1) {
+                const int64_t at = at1 + 2 * j + b;
+                p.y[at] = f32_to_f16_bits(fmaf(acc[j][b + 2], q1, __half2float(__ushort_as_half(p.base[at]))));
+              }
+            }
+          }
+        }
       }
     }
-    }
-  }
   }
 }
 
@@ -753,10 +754,10 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         const int top = max((rank + 15) & ~15, 16);
         for (int r = (warp - 2) * 64 + lane; r < (warp - 1) * 64; r += 32)
           for (int k = rank; k < top; k++) {
-            const uint32_t at = b_s + (s * KB + (k >> 6)) * kLtHalf + r * 128 + ((((k & 63) >> 3) ^ (r & 7)) << 4) +
-                                (k & 7) * 2;
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)0) : "memory");
-          }
+          const uint32_t at = b_s + (s * KB + (k >> 6)) * kLtHalf + r * 128 + ((((k & 63) >> 3) ^ (r & 7)) << 4) +
+                              (k & 7) * 2;
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)0) : "memory");
+        }
         fence_proxy_async_shared();
       }
       warp_arrive(fixd + 8 * s, lane);
@@ -849,7 +850,8 @@ __global__ void __launch_bounds__(kLtThreads, 1)
               ld256(w, bp + col);
             } else if (live && vec && col < left) {
               const uint4 v0 = *reinterpret_cast<const uint4*>(bp + col);
-              const uint4 v1 = col + 8 < left ? *reinterpret_cast<const uint4*>(bp + col + 8) : make_uint4(0u, 0u, 0u, 0u);
+              const uint4 v1 =
+                  col + 8 < left ? *reinterpret_cast<const uint4*>(bp + col + 8) : make_uint4(0u, 0u, 0u, 0u);
               w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w; w[4] = v1.x; w[5] = v1.y; w[6] = v1.z; w[7] = v1.w;
             } else {
 #pragma unroll

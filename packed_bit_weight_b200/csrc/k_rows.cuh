@@ -39,7 +39,7 @@ __device__ __forceinline__ int ld_dsmem_s32(const int* local, uint32_t r) {
 // One thread-block cluster (1 to 8 CTAs) does the whole sort, so it is one
 // launch and needs no workspace.  Every warp of the cluster owns one
 // contiguous run of pairs, which makes the order stable: it counts its ids
-// (lanes of equal id find each other with a warp vote, so no atomics), the
+// (lanes of equal id find each other with warp votes, so no atomics), the
 // CTA scans its warps' counts, the CTAs exchange their totals through
 // distributed shared memory, and a second walk over the same run writes each
 // pair's place.  ids outside [0, E) take no place; -1 says so on purpose
@@ -49,6 +49,19 @@ __device__ __forceinline__ int ld_dsmem_s32(const int* local, uint32_t r) {
 // RowTiles: the groups cut into tiles of at most T rows (equal ones of whole
 // 16-row steps), listed in group order, for kernels that give each tile a CTA.
 // ---------------------------------------------------------------------------
+// The lanes that hold the same valid id: one vote per bit of the ids (a match
+// over the warp costs a round per distinct id: the sort of 65,536 pairs over
+// 128 experts took 22 us with it, so 16).
+__device__ __forceinline__ unsigned same_id(int e, bool valid, int bits) {
+  unsigned m = __ballot_sync(0xFFFFFFFFu, valid);
+  for (int b = 0; b < bits; b++) {
+    const bool on = (e >> b) & 1;
+    const unsigned v = __ballot_sync(0xFFFFFFFFu, on);
+    m &= on ? v : ~v;
+  }
+  return m;
+}
+
 struct RowTile {  // rows perm[start] .. perm[start + count - 1] of group g
   int g, start, count, pad;
 };
@@ -78,14 +91,24 @@ __global__ void __launch_bounds__(kRowsSortThreads, 1)
   const int steps = (P + C * kRowsSortThreads - 1) / (C * kRowsSortThreads);  // 32-pair steps per warp
   const int64_t p0 = (int64_t)(c * kRowsSortWarps + warp) * steps * 32;
   int* mine = cnt + warp * E;
+  const int bits = 32 - __clz(E - 1 | 1);
   bool bad = false;
+  auto id_at = [&](int i) {  // this lane's id of step i (read four steps ahead of its use below)
+    const int64_t p = p0 + i * 32 + lane;
+    return i < steps && p < P ? ids[p] : -1;
+  };
+  int ahead[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) ahead[j] = id_at(j);
+#pragma unroll 4
   for (int i = 0; i < steps; i++) {
     const int64_t p = p0 + i * 32 + lane;
-    int e = p < P ? ids[p] : -1;
+    int e = ahead[i & 3];
+    ahead[i & 3] = id_at(i + 4);
     bool valid = e >= 0 && e < E - rest;
     bad |= !valid && e != -1;
     if (rest && !valid && p < P) { e = E - 1; valid = true; }
-    const unsigned peers = __match_any_sync(0xFFFFFFFFu, valid ? e : -1);
+    const unsigned peers = same_id(e, valid, bits);
     if (valid && (peers & lt) == 0) mine[e] += __popc(peers);
     __syncwarp();
   }
@@ -156,12 +179,16 @@ __global__ void __launch_bounds__(kRowsSortThreads, 1)
     }
   }
   __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; j++) ahead[j] = id_at(j);
+#pragma unroll 4
   for (int i = 0; i < steps; i++) {
     const int64_t p = p0 + i * 32 + lane;
-    int e = p < P ? ids[p] : -1;
+    int e = ahead[i & 3];
+    ahead[i & 3] = id_at(i + 4);
     bool valid = e >= 0 && e < E - rest;
     if (rest && !valid && p < P) { e = E - 1; valid = true; }
-    const unsigned peers = __match_any_sync(0xFFFFFFFFu, valid ? e : -1);
+    const unsigned peers = same_id(e, valid, bits);
     int place = -1;
     if (valid) place = grand[e] + before[e] + mine[e] + __popc(peers & lt);
     __syncwarp();
