@@ -7,9 +7,10 @@
 // n (lora_token_kernel).  More rows: the rows are sorted by adapter into tiles
 // (the sort of k_rows.cuh), the middle products A x are taken per tile with the
 // cluster's CTAs and warps sharing k (lora_shrink_kernel), and B and base are
-// streamed once per tile (lora_expand_kernel).  The bound is bytes: A and B of
-// the adapters in use, x, base and y; the products are rank / (bytes) small,
-// so legacy MMAs straight from global memory, without staging, keep up.
+// streamed once per tile (lora_expand_kernel; lora_expand_tc_kernel for long
+// inputs).  The bound is bytes: A and B of the adapters in use, x, base and y.
+// The products are small beside them (rank times two operations a value), so
+// legacy MMAs keep up except at 512 rows and more of ranks above 32.
 #pragma once
 #include "k_ggemm.cuh"
 #include "k_rows.cuh"
@@ -17,7 +18,7 @@
 namespace qmm {
 
 constexpr int kLoraMaxRank = 256;
-constexpr int kLoraCluster = 8;    // CTAs that share a row (or a tile)
+constexpr int kLoraCluster = 8;    // CTAs that share a row; at most so many share a tile's k
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
 
