@@ -353,7 +353,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
     float s = 0.f;
 #pragma unroll 8
     for (int c = 0; c < cs; c++) s += ld_dsmem_f32(sh + i, (uint32_t)c);
-    p.h[(int64_t)(tile.start + (i >> 6)) * R + rb + r] = s;
+    // (0 past the rank, where the staged zeros times an infinity or NaN in x are NaN)
+    p.h[(int64_t)(tile.start + (i >> 6)) * R + rb + r] = rb + r < rank ? s : 0.f;
   }
   __syncwarp();
   cluster_sync();  // no CTA leaves while its partial sums are read

@@ -1,0 +1,65 @@
+"""Adapters whose values or ranks are out of the ordinary, on each of their
+paths (a cluster per row, sorted tiles, sorted tiles on tcgen05)."""
+import numpy as np
+import pytest
+import torch
+
+from packed_bit_weight_b200 import qmm
+from rows_util import lora, within
+
+pytestmark = pytest.mark.gpu
+
+# rows, rank of the pool and the kernel that they take
+PATHS = [(1, 64, "lora_token"), (70, 32, "lora_tiled"), (300, 64, "lora_tiled"), (300, 128, "lora_tiled"),
+         (80, 256, "lora_tiled"), (600, 48, "lora_tc"), (600, 128, "lora_tc")]
+
+
+def _c(a):
+    return None if a is None else torch.from_numpy(a).cuda()
+
+
+def _run(A, B, sc, rk, x, ids, base, path):
+    ad = qmm.Adapters(_c(A), _c(B), _c(sc), _c(rk))
+    ws = torch.full((qmm.qmm_lora_workspace_bytes(ad, ids.size),), 0x7F, dtype=torch.uint8, device="cuda")
+    y = torch.full(base.shape, 7.0, dtype=torch.float16, device="cuda")
+    qmm.qmm_lora(ad, _c(x), _c(ids), _c(base), y, ws=ws)
+    assert qmm.qmm_last_variant().startswith(path), qmm.qmm_last_variant()
+    y2 = _c(base)
+    qmm.qmm_lora(ad, _c(x), _c(ids), y2, y2, ws=ws)
+    assert torch.equal(y2.view(torch.int16), y.view(torch.int16))   # in place
+    assert qmm.qmm_sync_check() == 0
+    return y.cpu().numpy()
+
+
+def _definition(x, base, ids, A, B, sc, rk):
+    """(y, bound) in double; infinities and NaN have to be met exactly."""
+    d = lambda v: v.astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        y, bound = lora(d(x), d(base), ids, d(A), d(B), sc, rk)
+    return y, np.where(np.isfinite(y), bound, 0.0)
+
+
+@pytest.mark.parametrize("value", [np.inf, np.nan])
+@pytest.mark.parametrize("m,R,path", PATHS)
+def test_ranks_in_use_with_an_infinity_or_nan_in_x(m, R, path, value):
+    """What a rank leaves out adds nothing, whatever x holds: with positive
+    values an infinity in x gives +inf in every column of its row (base for a
+    rank of 0), and NaN gives NaN there (base for a rank of 0)."""
+    rng = np.random.default_rng(m + R)
+    ranks = np.unique([0, 1, 7, 8, 17, 24, R // 2 + 1, R - 8, R - 1, R]).astype(np.int32)
+    for shift in range(len(ranks) if m == 1 else 1):
+        rk = np.roll(ranks, -shift).copy()
+        L, n, k = rk.size, 136, 72
+        A, B = np.abs(rng.standard_normal((2, L, max(R, n), max(R, k)))).astype(np.float16) + np.float16(0.25)
+        A, B = np.ascontiguousarray(A[:, :R, :k]), np.ascontiguousarray(B[:, :n, :R])
+        sc = np.full(L, 0.5, np.float32)
+        x = (np.abs(rng.standard_normal((m, k))) + 0.25).astype(np.float16)
+        base = rng.standard_normal((m, n)).astype(np.float16)
+        ids = (np.arange(m) % L).astype(np.int32)
+        x[:: 2 if m > 1 else 1, 5] = value
+        y = _run(A, B, sc, rk, x, ids, base, path)
+        within(y, *_definition(x, base, ids, A, B, sc, rk), path)
+        hit = np.flatnonzero(~np.isfinite(x).all(axis=1))
+        none = rk[ids[hit]] == 0
+        assert np.array_equal(y[hit[none]], base[hit[none]])
+        assert (np.isnan(y[hit[~none]]) if np.isnan(value) else y[hit[~none]] == np.inf).all()
