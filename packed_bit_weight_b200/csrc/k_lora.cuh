@@ -400,6 +400,50 @@ __device__ __forceinline__ void h_split(float x, uint16_t& hi, uint16_t& lo) {
   lo = fabsf(back) <= 65504.f ? __half_as_ushort(__float2half_rn(x - back)) : (uint16_t)0;
 }
 
+// True if one of 8 fp16 values is an infinity or NaN (0 times it is NaN).
+__device__ __forceinline__ bool nonfinite8(const uint4& v) {
+  uint32_t acc;
+  asm("{\n .reg .b32 t;\n mul.rn.f16x2 t, %1, %5;\n fma.rn.f16x2 t, %2, %5, t;\n fma.rn.f16x2 t, %3, %5, t;\n"
+      " fma.rn.f16x2 %0, %4, %5, t;\n}"
+      : "=r"(acc)
+      : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(0u));
+  return (acc & 0x7FFF7FFFu) != 0u;
+}
+
+// 8 columns of a row of which the first `left` exist, value by value (rows that
+// do not start on 16 bytes).
+__device__ __forceinline__ uint4 load8(const uint16_t* p, int left) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    if (i < left) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(uint16_t* p, const uint4& v, int left) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    if (i < left) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+}
+
+// Columns c0 .. c1 - 1 of one row by one warp, in fp32 alone: y[c] =
+// fp16(base[c] + scale sum_r h[r] B[c][r]).  The products of two fp16 halves
+// give NaN where B holds an infinity (inf * hi + inf * lo, with lo 0 or of the
+// other sign), so outputs that come out infinite or NaN are not stored and are
+// taken again here.  Rare, so it reads h and B from global memory.
+__device__ __noinline__ void lora_row_fp32(uint16_t* y, const uint16_t* base, const float* h, const uint16_t* B, int R,
+                                           int rank, float scale, int c0, int c1) {
+  for (int c = c0 + (threadIdx.x & 31); c < c1; c += 32) {
+    float s = 0.f;
+    for (int r = 0; r < rank; r += 8) {
+      const float4 h0 = *reinterpret_cast<const float4*>(h + r), h1 = *reinterpret_cast<const float4*>(h + r + 4);
+      const float hv[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+      s = dot8f(mask8(*reinterpret_cast<const uint4*>(B + (int64_t)c * R + r), rank - r), hv, s);
+    }
+    y[c] = f32_to_f16_bits(fmaf(scale, s, __half2float(__ushort_as_half(base[c]))));
+  }
+}
+
 // CTAs per SM: what the registers of B's fragments (16 KC a thread) leave
 constexpr int lora_expand_ctas(int KC) { return KC <= 4 ? 2 : 1; }
 
@@ -509,6 +553,7 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
 #pragma unroll
           for (int c = 0; c < KC; c++) w[j][c] = mask8(w[j][c], rank - (32 * c + 8 * tig));
       }
+      unsigned redo = 0;  // this lane's pieces taken again in fp32: bits 2g, 2g + 1 for its two rows of group g
       for (int g0 = 0; g0 < groups; g0 += kAhead) {
 #pragma unroll
         for (int d = 0; d < kAhead; d++) {
@@ -517,7 +562,7 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
           const int i0 = g * 16 + grp, i1 = i0 + 8;
           const bool ok0 = i0 < tile.count, ok1 = i1 < tile.count;
           const int64_t at0 = yoff[ok0 ? i0 : 0] + col, at1 = yoff[ok1 ? i1 : 0] + col;
-          const uint4 b0 = ahead[d][0], b1 = ahead[d][1];
+          uint4 b0 = ahead[d][0], b1 = ahead[d][1];
           load_base(g + kAhead, ahead[d]);
           float acc[4][4];
 #pragma unroll
@@ -541,33 +586,39 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
           }
           // acc[j][0..1]: row i0, columns col + 2j, + 1; acc[j][2..3]: row i1
           const float q0 = factor[i0], q1 = factor[i1];
-          if (vec) {
-            const uint32_t bw0[4] = {b0.x, b0.y, b0.z, b0.w}, bw1[4] = {b1.x, b1.y, b1.z, b1.w};
-            uint32_t o0[4], o1[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-              const float2 f0 = f16x2_to_f32x2(bw0[j]), f1 = f16x2_to_f32x2(bw1[j]);
-              o0[j] = f32x2_to_f16x2(fmaf(acc[j][0], q0, f0.x), fmaf(acc[j][1], q0, f0.y));
-              o1[j] = f32x2_to_f16x2(fmaf(acc[j][2], q1, f1.x), fmaf(acc[j][3], q1, f1.y));
-            }
-            if (ok0 && col < c1) *reinterpret_cast<uint4*>(p.y + at0) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-            if (ok1 && col < c1) *reinterpret_cast<uint4*>(p.y + at1) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-#pragma unroll
-              for (int b = 0; b < 2; b++) {
-              if (col + 2 * j + b >= c1) continue;
-              if (ok0) {
-                const int64_t at = at0 + 2 * j + b;
-                p.y[at] = f32_to_f16_bits(fmaf(acc[j][b], q0, __half2float(__ushort_as_half(p.base[at]))));
-              }
-              if (ok1) {
-                const int64_t at = at1 + 2 * j + b;
-                p.y[at] = f32_to_f16_bits(fmaf(acc[j][b + 2], q1, __half2float(__ushort_as_half(p.base[at]))));
-              }
-            }
+          if (!vec) {
+            if (ok0) b0 = load8(p.base + at0, c1 - col);
+            if (ok1) b1 = load8(p.base + at1, c1 - col);
           }
+          const uint32_t bw0[4] = {b0.x, b0.y, b0.z, b0.w}, bw1[4] = {b1.x, b1.y, b1.z, b1.w};
+          uint32_t o0[4], o1[4];
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const float2 f0 = f16x2_to_f32x2(bw0[j]), f1 = f16x2_to_f32x2(bw1[j]);
+            o0[j] = f32x2_to_f16x2(fmaf(acc[j][0], q0, f0.x), fmaf(acc[j][1], q0, f0.y));
+            o1[j] = f32x2_to_f16x2(fmaf(acc[j][2], q1, f1.x), fmaf(acc[j][3], q1, f1.y));
+          }
+          const uint4 v0 = make_uint4(o0[0], o0[1], o0[2], o0[3]), v1 = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+          // a piece that is infinite or NaN somewhere is left for lora_row_fp32
+          const bool on0 = ok0 && col < c1, on1 = ok1 && col < c1;
+          const bool bad0 = on0 && nonfinite8(v0), bad1 = on1 && nonfinite8(v1);
+          redo |= (bad0 ? 1u : 0u) << (2 * g) | (bad1 ? 2u : 0u) << (2 * g);
+          if (on0 && !bad0) {
+            if (vec) *reinterpret_cast<uint4*>(p.y + at0) = v0;
+            else store8(p.y + at0, v0, c1 - col);
+          }
+          if (on1 && !bad1) {
+            if (vec) *reinterpret_cast<uint4*>(p.y + at1) = v1;
+            else store8(p.y + at1, v1, c1 - col);
+          }
+        }
+      }
+      for (unsigned todo = __ballot_sync(0xFFFFFFFFu, redo != 0); todo; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1, cf = nb + 8 * (from & 3);
+        for (unsigned m = __shfl_sync(0xFFFFFFFFu, redo, from); m; m &= m - 1) {
+          const int bit = __ffs(m) - 1, i = (bit >> 1) * 16 + (bit & 1) * 8 + (from >> 2);
+          lora_row_fp32(p.y + yoff[i], p.base + yoff[i], p.h + (int64_t)(tile.start + i) * R, B, R, rank, scale, cf,
+                        min(cf + 8, c1));
         }
       }
     }
@@ -868,37 +919,51 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         if (!ok) { s_abort = 1; break; }
         tc_fence_after();
         if (32 * q < tile.count) {
+          unsigned redo = 0;  // this row's pieces of 16 columns that are infinite or NaN somewhere, for lora_row_fp32
 #pragma unroll
           for (int j = 0; j < 4; j++) {
             uint32_t r[32];
             tmem_ld32(tmem + 128u * a + 32u * j + ((uint32_t)(32 * q) << 16), r);
             tmem_ld_wait();
-            if (!live) continue;
-            if (vec) {
 #pragma unroll
-              for (int i = 0; i < 2; i++) {
-                const int col = 32 * j + 16 * i;
-                uint32_t o[8];
+            for (int i = 0; i < 2; i++) {
+              const int col = 32 * j + 16 * i;
+              if (!vec && live) {
+                uint32_t(&w)[8] = *reinterpret_cast<uint32_t(*)[8]>(&bv[j & 1][8 * i]);
+                const uint4 v0 = load8(bp + col, left - col), v1 = load8(bp + col + 8, left - col - 8);
+                w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w; w[4] = v1.x; w[5] = v1.y; w[6] = v1.z; w[7] = v1.w;
+              }
+              uint32_t o[8];
 #pragma unroll
-                for (int x = 0; x < 8; x++) {
-                  const float2 b = f16x2_to_f32x2(bv[j & 1][8 * i + x]);
-                  o[x] = f32x2_to_f16x2(fmaf(__uint_as_float(r[16 * i + 2 * x]), f, b.x),
-                                        fmaf(__uint_as_float(r[16 * i + 2 * x + 1]), f, b.y));
-                }
+              for (int x = 0; x < 8; x++) {
+                const float2 b = f16x2_to_f32x2(bv[j & 1][8 * i + x]);
+                o[x] = f32x2_to_f16x2(fmaf(__uint_as_float(r[16 * i + 2 * x]), f, b.x),
+                                      fmaf(__uint_as_float(r[16 * i + 2 * x + 1]), f, b.y));
+              }
+              const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
+              const bool on = live && col < left;
+              const bool bad = on && (nonfinite8(v0) || nonfinite8(v1));
+              if (on && !bad) {
                 if (wide) {
-                  if (col < left) st256(yp + col, o);
+                  st256(yp + col, o);
+                } else if (vec) {
+                  *reinterpret_cast<uint4*>(yp + col) = v0;
+                  if (col + 8 < left) *reinterpret_cast<uint4*>(yp + col + 8) = v1;
                 } else {
-                  if (col < left) *reinterpret_cast<uint4*>(yp + col) = make_uint4(o[0], o[1], o[2], o[3]);
-                  if (col + 8 < left) *reinterpret_cast<uint4*>(yp + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                  store8(yp + col, v0, left - col);
+                  store8(yp + col + 8, v1, left - col - 8);
                 }
               }
-              if (j + 2 < 4) load_base(j + 2, bv[j & 1]);
-            } else {
-#pragma unroll
-              for (int x = 0; x < 32; x++)
-                if (32 * j + x < left)
-                  yp[32 * j + x] = f32_to_f16_bits(
-                      fmaf(__uint_as_float(r[x]), f, __half2float(__ushort_as_half(bp[32 * j + x]))));
+              redo |= (bad ? 1u : 0u) << (2 * j + i);
+            }
+            if (j + 2 < 4) load_base(j + 2, bv[j & 1]);
+          }
+          for (unsigned todo = __ballot_sync(0xFFFFFFFFu, redo != 0); todo; todo &= todo - 1) {
+            const int from = __ffs(todo) - 1, i = 32 * q + from;
+            for (unsigned m = __shfl_sync(0xFFFFFFFFu, redo, from); m; m &= m - 1) {
+              const int cf = c0 + 16 * (__ffs(m) - 1);
+              lora_row_fp32(p.y + yoff[tb][i], p.base + yoff[tb][i], p.h + (int64_t)(tile.start + i) * R,
+                            lora_b(p, tile.g), R, lora_rank(p, tile.g), scale, cf, min(cf + 16, n));
             }
           }
         }

@@ -63,3 +63,30 @@ def test_ranks_in_use_with_an_infinity_or_nan_in_x(m, R, path, value):
         none = rk[ids[hit]] == 0
         assert np.array_equal(y[hit[none]], base[hit[none]])
         assert (np.isnan(y[hit[~none]]) if np.isnan(value) else y[hit[~none]] == np.inf).all()
+
+
+@pytest.mark.parametrize("n", [401, 408, 416])
+@pytest.mark.parametrize("m,R,path", PATHS)
+def test_infinities_and_nan_in_b(m, R, path, n):
+    """An infinity in B gives an infinity of h's sign in its column (NaN where
+    two of opposite sign or 0 * inf meet), NaN gives NaN, and the other columns
+    are what they were."""
+    rng = np.random.default_rng(2 * m + R)
+    L, k = 2, 72
+    A = (rng.standard_normal((L, R, k)) * 0.1).astype(np.float16)
+    B = rng.standard_normal((L, n, R)).astype(np.float16)
+    cols = []
+    for c in (3, 395):
+        B[:, c, 1], B[:, c + 1, R - 1], B[:, c + 2, 3] = np.inf, -np.inf, np.nan
+        B[:, c + 3, 0], B[:, c + 3, 1] = np.inf, np.inf
+        cols += range(c, c + 4)
+    sc = np.array([0.5, 2.0], np.float32)
+    x, base = rng.standard_normal((m, k)).astype(np.float16), rng.standard_normal((m, n)).astype(np.float16)
+    ids = (np.arange(m) % L).astype(np.int32)
+    if m > 1:
+        x[m - 1] = 0                       # h = 0: 0 * inf
+    y = _run(A, B, sc, None, x, ids, base, path)
+    ref, bound = _definition(x, base, ids, A, B, sc, None)
+    within(y, ref, bound, path)
+    assert np.isinf(y[0, [3, 4, 395, 396]]).all() and np.isnan(y[:, [5, 397]]).all()
+    assert np.isfinite(np.delete(y, cols, 1)).all()
