@@ -454,8 +454,9 @@ typedef struct {
 /* The adapters of many requests at once, beside a shared projection: for
  * every row i with adapter a = adapter_ids[i],
  *   y[i] = fp16(base[i] + scales[a] * B_a (A_a x[i])),
- * both sums in fp32, one rounding; y[i] = base[i] for rows without an
- * adapter.  base is the projection's output (qmm_gemv, qmm_gemm); y may be
+ * both sums in fp32 (A x enters the second as two fp16 halves where more than a
+ * few rows are multiplied at once: each of its values keeps 22 bits), one
+ * rounding to fp16; y[i] = base[i] for rows without an adapter.  base is the projection's output (qmm_gemv, qmm_gemm); y may be
  * the same buffer.
  *   x            device, [m][k] fp16
  *   adapter_ids  device, [m] int32 in any order; -1 is a row without an

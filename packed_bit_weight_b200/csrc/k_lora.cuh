@@ -367,11 +367,18 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
 // there for all of the tile's rows; a warp's four n-tiles are interleaved so
 // that a lane's columns are 8 neighbours, one 16-byte piece of base and y.
 //
-// The middle product is held as two fp16 halves, h = 2^e (hi + lo): each row
-// is scaled by a power of two that brings its largest finite value to
-// [2^14, 2^15), hi is the rounded value and lo the rounded rest, so h keeps 22
-// bits (off by 2^-22 where one fp16 would be off by 2^-12) at twice the MMAs,
-// which the stream of base and y hides.
+// The middle product is held as two fp16 halves, h = 2^e (hi + 2^-12 lo): each
+// row is scaled by a power of two that brings its largest finite value to
+// [2^14, 2^15), hi is the rounded value and lo 2^12 times the rounded rest.  hi
+// is off by half a step, 2^-12 of a value of 2^-14 and more (2^-25 below), and lo
+// by 2^-12 of that rest or 2^-25, so a value of 2^-15 and more (2^-29 of the
+// row's largest) keeps 22 bits, at twice the MMAs of one fp16, which the stream
+// of base and y hides.  (With lo not scaled up its smallest step, 2^-24, took
+// bits from 2^-18 of the largest down.)  The products of lo come first, their
+// sum is multiplied by 2^-12, exactly, and the products of hi are added.  A row
+// with a smaller value in it (about one in 10^6 rows of rank 128 and normal
+// values) is taken by lora_row_fp32, and so is one whose scale and power of two
+// together leave fp32.
 // ---------------------------------------------------------------------------
 // Scale of a row of h held 32 values per register across the warp: f1 f2 =
 // 2^(14 - e) for the largest finite |value| in [2^e, 2^(e+1)) (two factors, so
@@ -392,12 +399,21 @@ __device__ __forceinline__ void h_scale(const float (&v)[N], float& f1, float& f
   f2 = __uint_as_float((uint32_t)(127 + (sh - (sh >> 1))) << 23);
   back = __uint_as_float((uint32_t)(127 - sh) << 23);
 }
-// x = hi + lo (+ 2^-22 |x|) as fp16 halves; an infinite or NaN hi has lo = 0.
+// x = hi + 2^-12 lo as fp16 halves; an infinite or NaN hi has lo = 0.
+constexpr int kLoraLoBits = 12;
 __device__ __forceinline__ void h_split(float x, uint16_t& hi, uint16_t& lo) {
   const __half h = __float2half_rn(x);
   const float back = __half2float(h);
   hi = __half_as_ushort(h);
-  lo = fabsf(back) <= 65504.f ? __half_as_ushort(__float2half_rn(x - back)) : (uint16_t)0;
+  lo = fabsf(back) <= 65504.f ? __half_as_ushort(__float2half_rn((x - back) * (float)(1 << kLoraLoBits))) : (uint16_t)0;
+}
+// A scaled value that the halves hold in fewer than 22 bits.
+__device__ __forceinline__ bool h_small(float x) { return x != 0.f && fabsf(x) < 0x1p-15f; }
+// scale * back, or NaN for a row that is left for lora_row_fp32, as its outputs
+// then show: here one whose factor alone is infinite.
+__device__ __forceinline__ float h_factor(float scale, float back) {
+  const float f = scale * back;
+  return fabsf(f) > 3.4028235e38f && fabsf(scale) <= 3.4028235e38f ? __uint_as_float(0x7FC00000u) : f;
 }
 
 // True if one of 8 fp16 values is an infinity or NaN (0 times it is NaN).
@@ -430,7 +446,8 @@ __device__ __forceinline__ void store8(uint16_t* p, const uint4& v, int left) {
 // fp16(base[c] + scale sum_r h[r] B[c][r]).  The products of two fp16 halves
 // give NaN where B holds an infinity (inf * hi + inf * lo, with lo 0 or of the
 // other sign), so outputs that come out infinite or NaN are not stored and are
-// taken again here.  Rare, so it reads h and B from global memory.
+// taken again here, and so are rows with a value that the halves hold in too few
+// bits.  Rare, so it reads h and B from global memory.
 __device__ __noinline__ void lora_row_fp32(uint16_t* y, const uint16_t* base, const float* h, const uint16_t* B, int R,
                                            int rank, float scale, int c0, int c1) {
   for (int c = c0 + (threadIdx.x & 31); c < c1; c += 32) {
@@ -447,7 +464,9 @@ __device__ __noinline__ void lora_row_fp32(uint16_t* y, const uint16_t* base, co
 // CTAs per SM: what the registers of B's fragments (16 KC a thread) leave
 constexpr int lora_expand_ctas(int KC) { return KC <= 4 ? 2 : 1; }
 
-template <int KC>  // 32-wide chunks of the rank: R <= 32 KC
+// KC: 32-wide chunks of the rank, R <= 32 KC.  VEC: rows of y are whole 16-byte
+// pieces (n % 8 == 0).
+template <int KC, bool VEC>
 __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expand_kernel(const LoraArgs p) {
   extern __shared__ __align__(16) uint4 frag[];  // [row group][chunk][step][hi, lo][lane] fragments of h
   __shared__ int64_t yoff[128];  // rows of base and y, in elements
@@ -474,7 +493,7 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
       __syncthreads();
       for (int i = warp; i < tile.count; i += kLoraWarps) {
         const int64_t at = yoff[i];
-        copy_span(p.y + at, p.base + at, c0, c1, (n & 7) == 0, lane, 32);
+        copy_span(p.y + at, p.base + at, c0, c1, VEC, lane, 32);
       }
       continue;
     }
@@ -491,12 +510,13 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
         for (int c = 0; c < KC; c++)
           v[r][c] = (i0 + r < tile.count && 32 * c + lane < R) ? p.h[(int64_t)(tile.start + i0 + r) * R + 32 * c + lane]
                                                                : 0.f;
+      unsigned few = 0;  // rows with a value of this lane that is too small
 #pragma unroll
       for (int r = 0; r < kAtOnce; r++) {
         const int i = i0 + r;
         float f1, f2, back;
         h_scale<KC>(v[r], f1, f2, back);
-        if (lane == 0) factor[i] = scale * back;
+        if (lane == 0) factor[i] = h_factor(scale, back);
         // column r = 32 c + 8 t + 4 s + 2 w + b of row i: word (row half) + 2 w of
         // lane (i % 8, t), step s of chunk c, half b
         const int t = lane >> 3, s = (lane >> 2) & 1, w = (lane >> 1) & 1, b = lane & 1;
@@ -505,16 +525,20 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
         for (int c = 0; c < KC; c++) {
           uint16_t hi, lo;
           h_split(v[r][c] * f1 * f2, hi, lo);
+          if (h_small(v[r][c] * f1 * f2)) few |= 1u << r;
           uint16_t* f = reinterpret_cast<uint16_t*>(frag + ((((i >> 4) * KC + c) * 2 + s) * 2) * 32 + to);
           f[word * 2 + b] = hi;
           f[32 * 8 + word * 2 + b] = lo;
         }
       }
+      __syncwarp();
+#pragma unroll
+      for (int r = 0; r < kAtOnce; r++)
+        if (few >> r & 1u) factor[i0 + r] = __uint_as_float(0x7FC00000u);
     }
     __syncthreads();
     const uint16_t* B = lora_b(p, tile.g);
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const bool vec = (n & 7) == 0;
     for (int nb = c0 + warp * 32; nb < c1; nb += kLoraWarps * 32) {
       uint4 w[4][KC];
 #pragma unroll
@@ -534,13 +558,13 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
       const int col = nb + 8 * tig;  // this lane's 8 columns
       // base, kAhead row groups ahead of its use (loads stay behind the stores
       // they follow: y may be base)
-      constexpr int kAhead = KC <= 4 ? 3 : 1;
+      constexpr int kAhead = KC == 1 ? 3 : KC <= 4 ? 2 : 1;  // (KC 2 and 4 meet tiles of two groups only)
       uint4 ahead[kAhead][2];
       auto load_base = [&](int g, uint4 (&v)[2]) {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
           const int i = g * 16 + grp + 8 * h;
-          v[h] = (vec && i < tile.count && col < c1)
+          v[h] = (VEC && i < tile.count && col < c1)
                      ? *reinterpret_cast<const uint4*>(p.base + yoff[i] + col)
                      : zero;
         }
@@ -570,23 +594,28 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
 #pragma unroll
             for (int c = 0; c < 4; c++) acc[j][c] = 0.f;
 #pragma unroll
-          for (int c = 0; c < KC; c++) {
-            if (32 * c >= rank) break;
+          for (int half = 1; half >= 0; half--) {  // lo, then hi
 #pragma unroll
-            for (int s = 0; s < 2; s++) {
-              const uint4* f = frag + (((g * KC + c) * 2 + s) * 2) * 32 + lane;
-              const uint4 hi = f[0], lo = f[32];
+            for (int c = 0; c < KC; c++) {
+              if (32 * c >= rank) break;
 #pragma unroll
-              for (int j = 0; j < 4; j++) {
-                const uint32_t v0 = s ? w[j][c].z : w[j][c].x, v1 = s ? w[j][c].w : w[j][c].y;
-                mma_16816(acc[j], hi.x, hi.y, hi.z, hi.w, v0, v1);
-                mma_16816(acc[j], lo.x, lo.y, lo.z, lo.w, v0, v1);
+              for (int s = 0; s < 2; s++) {
+                const uint4 hv = frag[((((g * KC + c) * 2 + s) * 2) + half) * 32 + lane];
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                  mma_16816(acc[j], hv.x, hv.y, hv.z, hv.w, s ? w[j][c].z : w[j][c].x, s ? w[j][c].w : w[j][c].y);
               }
+            }
+            if (half) {
+#pragma unroll
+              for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int c = 0; c < 4; c++) acc[j][c] *= 1.0f / (1 << kLoraLoBits);
             }
           }
           // acc[j][0..1]: row i0, columns col + 2j, + 1; acc[j][2..3]: row i1
           const float q0 = factor[i0], q1 = factor[i1];
-          if (!vec) {
+          if (!VEC) {
             if (ok0) b0 = load8(p.base + at0, c1 - col);
             if (ok1) b1 = load8(p.base + at1, c1 - col);
           }
@@ -604,11 +633,11 @@ __global__ void __launch_bounds__(kLoraThreads, lora_expand_ctas(KC)) lora_expan
           const bool bad0 = on0 && nonfinite8(v0), bad1 = on1 && nonfinite8(v1);
           redo |= (bad0 ? 1u : 0u) << (2 * g) | (bad1 ? 2u : 0u) << (2 * g);
           if (on0 && !bad0) {
-            if (vec) *reinterpret_cast<uint4*>(p.y + at0) = v0;
+            if (VEC) *reinterpret_cast<uint4*>(p.y + at0) = v0;
             else store8(p.y + at0, v0, c1 - col);
           }
           if (on1 && !bad1) {
-            if (vec) *reinterpret_cast<uint4*>(p.y + at1) = v1;
+            if (VEC) *reinterpret_cast<uint4*>(p.y + at1) = v1;
             else store8(p.y + at1, v1, c1 - col);
           }
         }
@@ -676,6 +705,16 @@ __device__ __forceinline__ void st256(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
                "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
+}
+
+// D = A B + 2^-BITS D
+template <int BITS>
+__device__ __forceinline__ void umma_f16_scaled_d(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, 1, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p, %4;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(BITS)
+      : "memory");
 }
 
 template <int KB>  // 64-wide k blocks: R <= 64 KB
@@ -778,8 +817,14 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           const uint32_t blk = (uint32_t)(kk >> 2) * kLtHalf;
           const uint64_t db = umma_desc_k128(b_s + s * KB * kLtHalf + blk) + (uint64_t)(2 * (kk & 3));
           const uint64_t dh = umma_desc_k128(h_s + blk) + (uint64_t)(2 * (kk & 3));
-          umma_f16(d, dh, db, idesc, kk != 0);
-          umma_f16(d, dh + (uint64_t)(KB * kLtHalf / 16), db, idesc, 1);
+          umma_f16(d, dh + (uint64_t)(KB * kLtHalf / 16), db, idesc, kk != 0);
+        }
+        for (int kk = 0; kk < k16; kk++) {
+          const uint32_t blk = (uint32_t)(kk >> 2) * kLtHalf;
+          const uint64_t db = umma_desc_k128(b_s + s * KB * kLtHalf + blk) + (uint64_t)(2 * (kk & 3));
+          const uint64_t dh = umma_desc_k128(h_s + blk) + (uint64_t)(2 * (kk & 3));
+          if (kk == 0) umma_f16_scaled_d<kLoraLoBits>(d, dh, db, idesc);
+          else umma_f16(d, dh, db, idesc, 1);
         }
         umma_commit(empty + 8 * s);
         umma_commit(accf + 8 * a);
@@ -861,22 +906,28 @@ __global__ void __launch_bounds__(kLtThreads, 1)
               v[r][b] = (i0 + r < tile.count && 32 * b + lane < R)
                             ? p.h[(int64_t)(tile.start + i0 + r) * R + 32 * b + lane]
                             : 0.f;
+          unsigned few = 0;  // rows with a value of this lane that is too small
 #pragma unroll
           for (int r = 0; r < 4; r++) {
             float f1, f2, back;
             h_scale<2 * KB>(v[r], f1, f2, back);
             const int i = i0 + r;
-            if (lane == 0) factor[tb][i] = scale * back;
+            if (lane == 0) factor[tb][i] = h_factor(scale, back);
 #pragma unroll
             for (int b = 0; b < 2 * KB; b++) {
               uint16_t hi, lo;
               h_split(v[r][b] * f1 * f2, hi, lo);
+              if (h_small(v[r][b] * f1 * f2)) few |= 1u << r;
               const int k = 32 * b + lane;
               const uint32_t at = h_s + (k >> 6) * kLtHalf + i * 128 + ((((k & 63) >> 3) ^ (i & 7)) << 4) + (k & 7) * 2;
               asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(hi) : "memory");
               asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + KB * kLtHalf), "h"(lo) : "memory");
             }
           }
+          __syncwarp();
+#pragma unroll
+          for (int r = 0; r < 4; r++)
+            if (few >> r & 1u) factor[tb][i0 + r] = __uint_as_float(0x7FC00000u);
         }
         fence_proxy_async_shared();
         warp_arrive(hfull, lane);

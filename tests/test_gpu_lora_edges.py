@@ -90,3 +90,29 @@ def test_infinities_and_nan_in_b(m, R, path, n):
     within(y, ref, bound, path)
     assert np.isinf(y[0, [3, 4, 395, 396]]).all() and np.isnan(y[:, [5, 397]]).all()
     assert np.isfinite(np.delete(y, cols, 1)).all()
+
+
+@pytest.mark.parametrize("ratio", [20, 30, 40, 43])
+@pytest.mark.parametrize("m,R,path", PATHS)
+def test_middle_products_of_very_different_sizes(m, R, path, ratio):
+    """A x of one rank 2^ratio times that of the others, and a B that leaves
+    the large one out: every value of A x is held as fp32 holds it, to 2^-21
+    of itself and not of the row's largest."""
+    rng = np.random.default_rng(m + R + ratio)
+    L, n, k = 1, 136, 64
+    A = np.zeros((L, R, k), np.float16)
+    A[0, :, : k // 2] = np.float16(2.0 ** -max(ratio - 29, 0)) * (1 + rng.random((R, k // 2))).astype(np.float16)
+    A[0, 0] = 0
+    A[0, 0, k // 2:] = 2.0 ** 8
+    x = (1 + rng.random((m, k))).astype(np.float16)
+    x[:, : k // 2] *= np.float16(2.0 ** -8)
+    x[:, k // 2:] = x[:, k // 2:] * np.float16(2.0 ** (min(ratio, 29) - 16))
+    B = rng.standard_normal((L, n, R)).astype(np.float16)
+    B[:, :, 0] = 0
+    sc = np.array([2.0 ** max(ratio - 29, 0)], np.float32)
+    base = np.zeros((m, n), np.float16)
+    ids = np.zeros(m, np.int32)
+    h = A[0].astype(np.float64) @ x[0].astype(np.float64)
+    assert 2.0 ** (ratio - 3) < h[0] / h[1:].max() < 2.0 ** (ratio + 3)
+    y = _run(A, B, sc, None, x, ids, base, path)
+    within(y, *_definition(x, base, ids, A, B, sc, None), path)
