@@ -471,7 +471,8 @@ typedef struct {
 qmm_status qmm_lora(const qmm_adapters* adapters, const uint16_t* x, const int32_t* adapter_ids, int64_t m,
                     const uint16_t* base, uint16_t* y, void* ws, size_t ws_bytes, void* stream);
 
-/* Device workspace bytes of qmm_lora for m rows (0 for sizes it refuses). */
+/* Device workspace bytes of qmm_lora for m rows (0 for sizes it refuses).  They
+ * never fall as m grows: a workspace for m rows serves any call of fewer. */
 size_t qmm_lora_workspace_bytes(const qmm_adapters* adapters, int64_t m);
 
 enum { QMM_OP_DEQUANT = 0, QMM_OP_GEMV = 1, QMM_OP_GEMM = 2, QMM_OP_ROUTE = 3, QMM_OP_GROUPED = 4,

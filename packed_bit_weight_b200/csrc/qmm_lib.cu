@@ -1618,12 +1618,13 @@ static bool lora_by_row(const qmm_adapters* ad, int64_t m) {
 // 2,048 rows of rank 16 40 / 46, rank 64 52 / 48, rank 128 89 / 52; 1,024 rows
 // of rank 64 31 / 29; 512 rows 20.6 / 20.5.
 static bool lora_tc(int64_t m, int64_t rank) { return m >= 512 && rank > 32 && rank <= 128; }
-static int lora_tile_rows(int64_t m, int64_t rank) { return lora_tc(m, rank) ? 128 : m >= 512 ? 64 : 32; }
-static int64_t lora_max_tiles(int64_t L, int64_t m, int64_t rank) {
-  return m / lora_tile_rows(m, rank) + std::min(m, L + 1);
-}
+constexpr int kLoraMinTile = 32;
+static int lora_tile_rows(int64_t m, int64_t rank) { return lora_tc(m, rank) ? 128 : m >= 512 ? 64 : kLoraMinTile; }
+static int64_t lora_max_tiles(int64_t L, int64_t m, int tile_rows) { return m / tile_rows + std::min(m, L + 1); }
 
-// Workspace of the tiled path: offsets, permutation, tile count, tiles, h.
+// Workspace of the tiled path: offsets, permutation, tile count, tiles, h.  The
+// list has room for the smallest tiles at every m, so that the size never falls
+// as m grows: one buffer serves all calls of fewer rows.
 struct LoraWorkspace {
   size_t offsets, perm, num, tiles, h, bytes;
 };
@@ -1633,7 +1634,7 @@ static LoraWorkspace lora_workspace(const qmm_adapters* ad, int64_t m) {
   w.perm = align256(4 * (size_t)(ad->num_adapters + 2));
   w.num = w.perm + align256(4 * (size_t)m);
   w.tiles = w.num + 256;
-  w.h = w.tiles + align256(sizeof(RowTile) * (size_t)lora_max_tiles(ad->num_adapters, m, ad->rank));
+  w.h = w.tiles + align256(sizeof(RowTile) * (size_t)lora_max_tiles(ad->num_adapters, m, kLoraMinTile));
   w.bytes = w.h + align256(4 * (size_t)m * (size_t)ad->rank);
   return w;
 }
@@ -1698,7 +1699,7 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
   a.num_tiles = reinterpret_cast<int32_t*>(base_ws + w.num);
   a.tiles = reinterpret_cast<RowTile*>(base_ws + w.tiles);
   a.h = reinterpret_cast<float*>(base_ws + w.h);
-  const int64_t tiles = lora_max_tiles(ad->num_adapters, m, ad->rank);
+  const int64_t tiles = lora_max_tiles(ad->num_adapters, m, lora_tile_rows(m, ad->rank));
   if (tiles * kLoraCluster > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
   const RowTiles rt = {a.tiles, a.num_tiles, lora_tile_rows(m, ad->rank), base == y};
   s = launch_route_rows(adapter_ids, m, ad->num_adapters + 1, 1, a.offsets, a.perm, nullptr, rt, st);
