@@ -1742,13 +1742,16 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
     return launch_status();
   }
   const int kc = (int)((ad->rank + 31) / 32), KC = kc <= 1 ? 1 : kc <= 2 ? 2 : kc <= 4 ? 4 : 8;
-  const int smem = (rt.T / 16) * KC * 4 * 32 * 16;
+  const int smem = (rt.T / 16) * KC * 4 * 32 * 16;  // (T <= 64)
   const bool vec = ad->n % 8 == 0;
   auto kern = vec ? lora_expand_kernel<8, true> : lora_expand_kernel<8, false>;
   if (KC == 1) kern = vec ? lora_expand_kernel<1, true> : lora_expand_kernel<1, false>;
   else if (KC == 2) kern = vec ? lora_expand_kernel<2, true> : lora_expand_kernel<2, false>;
   else if (KC == 4) kern = vec ? lora_expand_kernel<4, true> : lora_expand_kernel<4, false>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return QMM_ERR_CUDA;
+  // (the most of this instantiation, not this call's: the attribute is shared by
+  // the host threads, and another one may launch with 64-row tiles meanwhile)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * KC * 4 * 32 * 16) != cudaSuccess)
+    return QMM_ERR_CUDA;
   const int grid = lora_expand_ctas(KC) * di->sms;  // the CTAs that are resident at once
   if (launch_pdl(kern, dim3((unsigned)grid), dim3(kLoraThreads), (size_t)smem, st, a) != cudaSuccess)
     return QMM_ERR_CUDA;

@@ -1,5 +1,7 @@
 """Adapters whose values or ranks are out of the ordinary, on each of their
 paths (a cluster per row, sorted tiles, sorted tiles on tcgen05)."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -116,3 +118,40 @@ def test_middle_products_of_very_different_sizes(m, R, path, ratio):
     assert 2.0 ** (ratio - 3) < h[0] / h[1:].max() < 2.0 ** (ratio + 3)
     y = _run(A, B, sc, None, x, ids, base, path)
     within(y, *_definition(x, base, ids, A, B, sc, None), path)
+
+
+def test_two_host_threads_with_tiles_of_different_heights():
+    """Calls of one kernel instantiation with different amounts of shared
+    memory, from two host threads at once."""
+    rng = np.random.default_rng(1)
+    L, R, n, k = 2, 256, 264, 64
+    A, B = rng.standard_normal((L, R, k)).astype(np.float16), rng.standard_normal((L, n, R)).astype(np.float16)
+    ad = qmm.Adapters(_c(A), _c(B), _c(np.full(L, 0.05, np.float32)))
+    errors, jobs = [], []
+    for m in (300, 600):
+        x, base = _c(rng.standard_normal((m, k)).astype(np.float16)), _c(rng.standard_normal((m, n)).astype(np.float16))
+        ids = _c((np.arange(m) % L).astype(np.int32))
+        ws = torch.empty(qmm.qmm_lora_workspace_bytes(ad, m), dtype=torch.uint8, device="cuda")
+        want, y = torch.empty_like(base), torch.empty_like(base)
+        qmm.qmm_lora(ad, x, ids, base, want, ws=ws)
+        jobs.append((x, ids, base, y, ws, want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(x, ids, base, y, ws, want, stream):
+        try:
+            torch.cuda.set_device(0)
+            for _ in range(3000):
+                qmm.qmm_lora(ad, x, ids, base, y, ws=ws, stream=stream)
+        except Exception as e:                                 # noqa: BLE001 (shown below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for j in jobs:
+        assert torch.equal(j[3], j[5])
+    assert qmm.qmm_sync_check() == 0
