@@ -624,8 +624,14 @@ static qmm_status launch_iq4_tile_cfg(const qmm_weights* w0, const qmm_weights* 
   if (ids && P > kIqtMaxPairs) return QMM_ERR_UNSUPPORTED_SHAPE;
   if (grid < 1 || grid > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
   auto kern = iq4_tile_kernel<MODE, S, SPW, kMaxReg, W16, STG>;
-  const uint32_t smem = iqt_smem_bytes(S, wpc) + (STG ? (uint32_t)S * 16u * (uint32_t)(w0->k / 32 * 18) : 0u);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  auto smem_of = [](int warps) {  // k = warps * SPW * 128
+    return iqt_smem_bytes(S, warps) + (STG ? (uint32_t)S * 16u * (uint32_t)(warps * SPW * 72) : 0u);
+  };
+  const uint32_t smem = smem_of(wpc);
+  // (the most of this instantiation, not this call's: the attribute is shared by
+  // the host threads, and another one may launch with a longer k meanwhile)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem_of(iqt_max_threads(kMaxReg) / 32)) != cudaSuccess)
     return QMM_ERR_CUDA;
   IqtArgs a;
   a.data0 = static_cast<const uint8_t*>(w0->data);
