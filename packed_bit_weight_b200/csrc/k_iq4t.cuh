@@ -234,7 +234,9 @@ __device__ __forceinline__ void iqt_load(uint32_t (&w)[SPW][S][2][6], const uint
 }
 
 // Threads a CTA of this register budget may have.
-__host__ __device__ constexpr int iqt_max_threads(int maxreg) { return (65536 / maxreg) & ~31; }
+// (A quarter of the registers belongs to each of the SM's four schedulers, whose
+// warps take theirs whole: 96 registers leave 4 x 5 warps, not 21.)
+__host__ __device__ constexpr int iqt_max_threads(int maxreg) { return 4 * 32 * (65536 / 4 / (32 * maxreg)); }
 
 // In-kernel routing (a.ids): warp 0 collects the pairs p whose id is this
 // CTA's expert, in increasing p (the order of the stable routing sort), into

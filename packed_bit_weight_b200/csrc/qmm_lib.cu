@@ -674,7 +674,7 @@ static qmm_status launch_iq4_tile_cfg(const qmm_weights* w0, const qmm_weights* 
   return launch_status();
 }
 
-// Needs k % 256 == 0 and k <= 5376 (at most 21 warps of two super-steps)
+// Needs k % 256 == 0 and k <= 5120 (at most 20 warps of two super-steps)
 // or k % 128 == 0 and k <= 2048 (at most 16 warps of one); returns
 // QMM_ERR_UNSUPPORTED_SHAPE, having launched nothing, otherwise.
 template <int MODE>
