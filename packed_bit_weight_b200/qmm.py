@@ -529,12 +529,17 @@ class Adapters:
     scales: torch.Tensor
     ranks: torch.Tensor | None = None
 
+    def __setattr__(self, name, value):
+        # a new tensor is checked again, also where it lies at the old one's address
+        self.__dict__.pop("_desc", None)
+        self.__dict__[name] = value
+
     def desc(self) -> qmm_adapters:
-        """The C descriptor, rebuilt only when a tensor was replaced or moved
-        or another device became current."""
+        """The C descriptor, rebuilt only when a tensor was replaced, moved or
+        reshaped or another device became current."""
         a, b, s, r = self.a, self.b, self.scales, self.ranks
-        key = (a.data_ptr(), b.data_ptr(), s.data_ptr(), 0 if r is None else r.data_ptr(), a.shape, b.shape,
-               a.stride(), b.stride(), s.numel(), a.get_device(), _dev())
+        key = (a.data_ptr(), b.data_ptr(), s.data_ptr(), a.shape, b.shape, s.shape, a.stride(), b.stride(), s.stride(),
+               None if r is None else (r.data_ptr(), r.shape, r.stride()), _dev())
         cached = self.__dict__.get("_desc")
         if cached is not None and cached[0] == key:
             return cached[1]

@@ -155,3 +155,29 @@ def test_two_host_threads_with_tiles_of_different_heights():
     for j in jobs:
         assert torch.equal(j[3], j[5])
     assert qmm.qmm_sync_check() == 0
+
+
+def test_a_replaced_tensor_at_the_same_address_is_checked_again():
+    """Only descriptors are built here: nothing is launched."""
+    L, R, n, k = 4, 16, 64, 128
+    z = lambda *s, dt=torch.float16: torch.zeros(*s, dtype=dt, device="cuda")
+    ad = qmm.Adapters(z(L, R, k), z(L, n, R), z(L, dt=torch.float32), z(L, dt=torch.int32))
+    good = ad.desc()
+    for name, other in (("ranks", ad.ranks[:L - 1]), ("ranks", ad.ranks.view(torch.int64)),
+                        ("ranks", ad.ranks.view(torch.int16).view(2, L)[:1].expand(2, L)),
+                        ("scales", ad.scales[:L - 1]), ("scales", ad.scales.view(torch.float64)),
+                        ("scales", ad.scales[:1].expand(L)), ("ranks", ad.ranks[:1].expand(L)),
+                        ("a", ad.a.view(torch.int8)[..., :k]), ("b", ad.b.view(torch.int8)[..., :R])):
+        kept = getattr(ad, name)
+        assert other.data_ptr() == kept.data_ptr()
+        setattr(ad, name, other)
+        with pytest.raises(ValueError):
+            ad.desc()
+        setattr(ad, name, kept)
+        d = ad.desc()
+        assert (d.a, d.b, d.scales, d.ranks) == (good.a, good.b, good.scales, good.ranks)
+    short = ad.ranks
+    ad.desc()
+    short.resize_(L - 1)                       # (in place: the same object)
+    with pytest.raises(ValueError):
+        ad.desc()
