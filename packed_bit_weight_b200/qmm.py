@@ -405,6 +405,14 @@ def _here(t: torch.Tensor | None, esize: int | None, name: str, dev: int):
     raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, dev))
 
 
+def _half(t: torch.Tensor | None, name: str, dev: int):
+    """The address of a tensor of fp16 values that are calculated with:
+    torch.float16, or a 16-bit integer type that holds their bits."""
+    if t is not None and t.dtype is torch.bfloat16:
+        raise ValueError("%s is bfloat16; fp16 values (or their bits as int16) are expected" % name)
+    return _here(t, 2, name, dev)
+
+
 def _weights_here(w: PackedWeights, dev: int) -> None:
     _here(w.data, None, "data", dev)
     _here(w.scales, None, "scales", dev)
@@ -445,7 +453,8 @@ def _need_rows(rows: torch.Tensor, tok: torch.Tensor, tok_name: str, sorted_rows
 
 
 def qmm_permute(x: torch.Tensor, rows: torch.Tensor, xs: torch.Tensor, stream=None) -> torch.Tensor:
-    """xs[rows[t][s]] = x[t]: x [t][d] -> xs [t*topk][d]."""
+    """xs[rows[t][s]] = x[t]: x [t][d] -> xs [t*topk][d] (any 2-byte type: the
+    values are copied)."""
     t, topk, d = _need_rows(rows, x, "x", ((xs, "xs"),))
     dev = _dev()
     _check(_lib().qmm_permute(_here(x, 2, "x", dev), _here(rows, 4, "rows", dev), t, topk, d, _here(xs, 2, "xs", dev),
@@ -457,8 +466,8 @@ def qmm_permute_backward(dxs: torch.Tensor, rows: torch.Tensor, dx: torch.Tensor
     """dx[t] = sum_s dxs[rows[t][s]]: the gradient of qmm_permute."""
     t, topk, d = _need_rows(rows, dx, "dx", ((dxs, "dxs"),))
     dev = _dev()
-    _check(_lib().qmm_permute_backward(_here(dxs, 2, "dxs", dev), _here(rows, 4, "rows", dev), t, topk, d,
-                                       _here(dx, 2, "dx", dev), _stream_on(stream, dev)), "qmm_permute_backward")
+    _check(_lib().qmm_permute_backward(_half(dxs, "dxs", dev), _here(rows, 4, "rows", dev), t, topk, d,
+                                       _half(dx, "dx", dev), _stream_on(stream, dev)), "qmm_permute_backward")
     return dx
 
 
@@ -468,8 +477,8 @@ def qmm_unpermute(ys: torch.Tensor, rows: torch.Tensor, topk_weights: torch.Tens
     None): ys [t*topk][d] -> out [t][d]."""
     t, topk, d = _need_rows(rows, out, "out", ((ys, "ys"),), ((topk_weights, "topk_weights"),))
     dev = _dev()
-    _check(_lib().qmm_unpermute(_here(ys, 2, "ys", dev), _here(rows, 4, "rows", dev),
-                                _here(topk_weights, 4, "topk_weights", dev), t, topk, d, _here(out, 2, "out", dev),
+    _check(_lib().qmm_unpermute(_half(ys, "ys", dev), _here(rows, 4, "rows", dev),
+                                _here(topk_weights, 4, "topk_weights", dev), t, topk, d, _half(out, "out", dev),
                                 _stream_on(stream, dev)), "qmm_unpermute")
     return out
 
@@ -481,9 +490,9 @@ def qmm_unpermute_backward(dout: torch.Tensor, ys: torch.Tensor, rows: torch.Ten
     t, topk, d = _need_rows(rows, dout, "dout", ((ys, "ys"), (dys, "dys")),
                             ((topk_weights, "topk_weights"), (dweights, "dweights")))
     dev = _dev()
-    _check(_lib().qmm_unpermute_backward(_here(dout, 2, "dout", dev), _here(ys, 2, "ys", dev),
+    _check(_lib().qmm_unpermute_backward(_half(dout, "dout", dev), _half(ys, "ys", dev),
                                          _here(rows, 4, "rows", dev), _here(topk_weights, 4, "topk_weights", dev),
-                                         t, topk, d, _here(dys, 2, "dys", dev), _here(dweights, 4, "dweights", dev),
+                                         t, topk, d, _half(dys, "dys", dev), _here(dweights, 4, "dweights", dev),
                                          _stream_on(stream, dev)), "qmm_unpermute_backward")
     return dys, dweights
 
@@ -497,8 +506,8 @@ def qmm_grouped_gemm(w: PackedWeights, xs: torch.Tensor, offsets: torch.Tensor, 
     _need(offsets, 4 * (w.experts + 1), "offsets")
     dev = _dev()
     _weights_here(w, dev)
-    _check(_lib().qmm_grouped_gemm(ctypes.byref(d), _here(xs, 2, "xs", dev), _here(offsets, 4, "offsets", dev),
-                                   xs.shape[0], _here(ys, 2, "ys", dev), _stream_on(stream, dev)), "qmm_grouped_gemm")
+    _check(_lib().qmm_grouped_gemm(ctypes.byref(d), _half(xs, "xs", dev), _here(offsets, 4, "offsets", dev),
+                                   xs.shape[0], _half(ys, "ys", dev), _stream_on(stream, dev)), "qmm_grouped_gemm")
     return ys
 
 
@@ -512,8 +521,8 @@ def qmm_grouped_swiglu(gate: PackedWeights, up: PackedWeights, xs: torch.Tensor,
     dev = _dev()
     _weights_here(gate, dev)
     _weights_here(up, dev)
-    _check(_lib().qmm_grouped_swiglu(ctypes.byref(dg), ctypes.byref(du), _here(xs, 2, "xs", dev),
-                                     _here(offsets, 4, "offsets", dev), xs.shape[0], _here(h, 2, "h", dev),
+    _check(_lib().qmm_grouped_swiglu(ctypes.byref(dg), ctypes.byref(du), _half(xs, "xs", dev),
+                                     _here(offsets, 4, "offsets", dev), xs.shape[0], _half(h, "h", dev),
                                      _stream_on(stream, dev)), "qmm_grouped_swiglu")
     return h
 
@@ -565,6 +574,8 @@ class Adapters:
         d = qmm_adapters()
         d.num_adapters, d.n, d.k, d.rank = L, n, k, R
         for t, name in ((a, "a"), (b, "b")):
+            if t.dtype is torch.bfloat16:
+                raise ValueError("%s is bfloat16; fp16 values (or their bits as int16) are expected" % name)
             if not t.is_cuda:
                 raise ValueError("%s must be a CUDA tensor" % name)
             if t.element_size() != 2:
@@ -592,8 +603,8 @@ def qmm_lora(adapters: Adapters, x: torch.Tensor, adapter_ids: torch.Tensor, bas
     _need(y, 2 * m * n, "y")
     dev = _dev()
     wb = 0 if ws is None else ws.nbytes
-    _check(_lib().qmm_lora(adapters._ref(), _here(x, 2, "x", dev), _here(adapter_ids, 4, "adapter_ids", dev), m,
-                           _here(base, 2, "base", dev), _here(y, 2, "y", dev), _here(ws, None, "ws", dev), wb,
+    _check(_lib().qmm_lora(adapters._ref(), _half(x, "x", dev), _here(adapter_ids, 4, "adapter_ids", dev), m,
+                           _half(base, "base", dev), _half(y, "y", dev), _here(ws, None, "ws", dev), wb,
                            _stream_on(stream, dev)), "qmm_lora")
     return y
 

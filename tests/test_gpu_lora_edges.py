@@ -181,3 +181,30 @@ def test_a_replaced_tensor_at_the_same_address_is_checked_again():
     short.resize_(L - 1)                       # (in place: the same object)
     with pytest.raises(ValueError):
         ad.desc()
+
+
+def test_bfloat16_is_refused_in_every_place():
+    """With everything else on the GPU and right, one bfloat16 tensor at a time."""
+    z = lambda *s, dt=torch.float16: torch.zeros(*s, dtype=dt, device="cuda")
+    rows, off, g = z(8, 2, dt=torch.int32), z(3, dt=torch.int32), z(8, 2, dt=torch.float32)
+    db = qmm.qmm_data_bytes(1, 64, 256)
+    w = qmm.PackedWeights(1, 64, 256, torch.zeros(2 * db, dtype=torch.uint8, device="cuda"), None, 1.0, 2)
+    ad = qmm.Adapters(z(2, 16, 64), z(2, 64, 16), z(2, dt=torch.float32))
+    ids = z(8, dt=torch.int32)
+    calls = [
+        (lambda a, b: qmm.qmm_permute_backward(a, rows, b), [(16, 64), (8, 64)]),
+        (lambda a, b: qmm.qmm_unpermute(a, rows, g, b), [(16, 64), (8, 64)]),
+        (lambda a, b, c: qmm.qmm_unpermute_backward(a, b, rows, g, c, g.clone()), [(8, 64), (16, 64), (16, 64)]),
+        (lambda a, b: qmm.qmm_grouped_gemm(w, a, off, b), [(8, 256), (8, 64)]),
+        (lambda a, b: qmm.qmm_grouped_swiglu(w, w, a, off, b), [(8, 256), (8, 64)]),
+        (lambda a, b, c: qmm.qmm_lora(ad, a, ids, b, c), [(8, 64), (8, 64), (8, 64)]),
+        (lambda a, b: qmm.Adapters(a, b, ad.scales).desc(), [(2, 16, 64), (2, 64, 16)]),
+    ]
+    for fn, shapes in calls:
+        for dt in (torch.float16, torch.int16):
+            fn(*[z(*s, dt=dt) for s in shapes])
+        for i in range(len(shapes)):
+            with pytest.raises(ValueError, match="bfloat16"):
+                fn(*[z(*s, dt=torch.bfloat16 if j == i else torch.float16) for j, s in enumerate(shapes)])
+    qmm.qmm_permute(z(8, 64, dt=torch.bfloat16), rows, z(16, 64, dt=torch.bfloat16))   # copied
+    assert qmm.qmm_sync_check() == 0
