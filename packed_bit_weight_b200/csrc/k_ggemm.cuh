@@ -101,6 +101,28 @@ __device__ __forceinline__ bool gg_wait(uint32_t bar, uint32_t parity) {
   return mbar_wait(bar, parity);
 }
 
+// gg_wait of a whole warp, with one answer for all its lanes: on the fast path
+// none, a lane at a time only if one runs out of polls.
+__device__ __forceinline__ bool gg_wait_warp(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; i++)
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+}
+
+// Predicated stores: where a warp-wide instruction (tcgen05.ld) follows, the
+// lanes must not part for their stores.  (Joining them again by a barrier takes
+// 2 to 3 % of the grouped product: it holds the next load behind the stores.)
+__device__ __forceinline__ void st128_if(bool on, void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %0, 0;\n @p st.global.v4.b32 [%1], {%2,%3,%4,%5};\n}" ::"r"(
+                   (uint32_t)on),
+               "l"(p), "r"(a), "r"(b), "r"(c), "r"(d));
+}
+__device__ __forceinline__ void st16_if(bool on, void* p, uint32_t v) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %0, 0;\n @p st.global.b16 [%1], %2;\n}" ::"r"((uint32_t)on), "l"(p),
+               "h"((unsigned short)v));
+}
+
 // One arrival for a whole warp, once all its lanes are done (128 threads
 // arriving on one barrier one after another took longer than a k step).
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
@@ -245,14 +267,12 @@ __device__ __forceinline__ void gg_store(const uint32_t (&p)[4 * NR], int lane, 
   for (int i = 0; i < NR; i++) {
     const int r8 = 8 * i + (lane & 7);
     const int row = NR == 4 ? r8 : 2 * r8 + (lane >> 4);
-    if (row >= left) continue;
     uint16_t* yp = y + (int64_t)row * n + col;
-    if (vec && col + 8 <= n) {
-      *reinterpret_cast<uint4*>(yp) = make_uint4(q4[i][0], q4[i][1], q4[i][2], q4[i][3]);
+    if (vec) {
+      st128_if(row < left && col < n, yp, q4[i][0], q4[i][1], q4[i][2], q4[i][3]);
     } else {
 #pragma unroll
-      for (int c = 0; c < 8; c++)
-        if (col + c < n) yp[c] = (uint16_t)(q4[i][c >> 1] >> (16 * (c & 1)));
+      for (int c = 0; c < 8; c++) st16_if(row < left && col + c < n, yp + c, q4[i][c >> 1] >> (16 * (c & 1)));
     }
   }
 }
@@ -510,7 +530,7 @@ __global__ void __launch_bounds__(kGgThreads, 1)
       const bool valid = (SWI ? n0 + ((row >> 5) << 4) + (row & 15) : n0 + row) < n;
       for (int cc = 0; cc < nck; cc++, ck++) {
         const int slot = ck % kGgSlots;
-        ok = gg_wait(cfull + 8 * slot, (uint32_t)(ck / kGgSlots) & 1u);
+        ok = gg_wait_warp(cfull + 8 * slot, (uint32_t)(ck / kGgSlots) & 1u);
         if (!ok) break;
         const int steps = min(kGemmChunkSteps, ksteps - cc * kGemmChunkSteps);
         if (group < steps) {
@@ -605,6 +625,7 @@ __global__ void __launch_bounds__(kGgThreads, 1)
 
   // teardown: no MMA of ours may still be using tensor memory
   if (warp == 1 && lane == 0) gg_wait(done_bar, 0);
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kRowsSortThreads, 1)
     }
     total[e] = run;
   }
+  __syncwarp();  // (a cluster barrier is warp-wide; the lanes have walked different numbers of experts)
   cluster_sync();
   for (int e = tid; e < E; e += kRowsSortThreads) {
     int all = 0, b = 0;
@@ -135,6 +136,7 @@ __global__ void __launch_bounds__(kRowsSortThreads, 1)
     grand[e] = all;
     before[e] = b;
   }
+  __syncwarp();
   cluster_sync();  // (also: no CTA leaves while another still reads its totals)
   if (warp == 0) {  // exclusive scan over the experts, and over their tiles
     const bool want = tiles.list && c == 0;
