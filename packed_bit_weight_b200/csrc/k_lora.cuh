@@ -78,6 +78,16 @@ __device__ __forceinline__ float dot8f(const uint4& u, const float (&h)[8], floa
   return s;
 }
 
+// Bad ids and ranks of a pool without products (rank 0 or k = 0, where y = base
+// is a copy) are reported all the same.
+__global__ void __launch_bounds__(256) lora_check_kernel(const LoraArgs p) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.m; i += (int64_t)gridDim.x * 256) {
+    const int a = p.ids[i];
+    if (a >= 0 && a < p.L) lora_rank(p, a);
+    else if (a != -1) raise_error(ERR_BAD_EXPERT);
+  }
+}
+
 // Elements of an 8-value piece that lie at or past `left` set to zero (what a
 // rank leaves out is never used, whatever it holds).
 __device__ __forceinline__ uint4 mask8(uint4 v, int left) {

@@ -1665,12 +1665,6 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
   const LoraWorkspace w = lora_workspace(ad, m);
   if (w.bytes && (!ws || ws_bytes < w.bytes)) return QMM_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (ad->rank == 0 || ad->k == 0) {  // empty sums
-    if (base != y && cudaMemcpyAsync(y, base, 2 * (size_t)m * (size_t)ad->n, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
-      return QMM_ERR_CUDA;
-    set_variant("lora_copy");
-    return QMM_OK;
-  }
   LoraArgs a = {};
   a.a = static_cast<const uint16_t*>(ad->a);
   a.b = static_cast<const uint16_t*>(ad->b);
@@ -1687,6 +1681,13 @@ qmm_status qmm_lora(const qmm_adapters* ad, const uint16_t* x, const int32_t* ad
   a.x = x;
   a.base = base;
   a.y = y;
+  if (ad->rank == 0 || ad->k == 0) {  // empty sums
+    if (base != y && cudaMemcpyAsync(y, base, 2 * (size_t)m * (size_t)ad->n, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
+      return QMM_ERR_CUDA;
+    lora_check_kernel<<<(unsigned)std::min<int64_t>((m + 255) / 256, di->sms), 256, 0, st>>>(a);
+    set_variant("lora_copy");
+    return launch_status();
+  }
   if (lora_by_row(ad, m)) {
     // parts of n per row, no fewer than 64 outputs each: one CTA an SM up to
     // four rows (every part computes the middle product again: at one row two

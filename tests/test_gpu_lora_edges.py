@@ -208,3 +208,24 @@ def test_bfloat16_is_refused_in_every_place():
                 fn(*[z(*s, dt=torch.bfloat16 if j == i else torch.float16) for j, s in enumerate(shapes)])
     qmm.qmm_permute(z(8, 64, dt=torch.bfloat16), rows, z(16, 64, dt=torch.bfloat16))   # copied
     assert qmm.qmm_sync_check() == 0
+
+
+@pytest.mark.parametrize("m", [3, 70, 600])
+@pytest.mark.parametrize("R,k", [(0, 64), (16, 0)])
+def test_bad_ids_and_ranks_are_reported_without_a_product(R, k, m):
+    """A pool of rank 0, or k = 0: y = base, and bad ids are still reported."""
+    n, L = 72, 3
+    z = lambda *s: torch.zeros(*s, dtype=torch.float16, device="cuda")
+    base = torch.randn(m, n, device="cuda").to(torch.float16)
+    for inplace in (False, True):
+        for bad_id, bad_rank in ((-1, False), (L, False), (-2, False), (0, True)):
+            ranks = torch.zeros(L, dtype=torch.int32, device="cuda")
+            if bad_rank:
+                ranks[0] = R + 1
+            ad = qmm.Adapters(z(L, R, k), z(L, n, R), torch.ones(L, device="cuda"), ranks)
+            ids = (torch.arange(m, device="cuda") % (L - 1) + 1).to(torch.int32)
+            ids[m - 1] = bad_id
+            y = base.clone() if inplace else torch.empty_like(base)
+            qmm.qmm_lora(ad, z(m, k), ids, y if inplace else base, y)
+            assert qmm.qmm_sync_check() == (0 if bad_id == -1 else 7)
+            assert torch.equal(y, base)
