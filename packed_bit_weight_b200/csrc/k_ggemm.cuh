@@ -228,13 +228,6 @@ __device__ __forceinline__ void gg_decode(uint32_t src, int row, bool valid, uin
   }
 }
 
-// SiLU(z) = z / (1 + e^-z) by the fast exponential and division: off by
-// 2 + 1.2 |z| and 2 fp32 steps, far below half an fp16 step of the result it
-// is rounded to.  (With the copies and the decode left out, gate and up of
-// 8,192 pairs took 147 us with expf and the IEEE division, one epilogue warp
-// per scheduler, and 78 us with these.)
-__device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
-
 // Store 32 rows of a warp's columns.  p[i] holds two columns of one row, its
 // number's bits by exchange: bit 0 of the lane has been exchanged for the
 // lowest bit of i.  Two more steps (lane bits 1 and 2) leave 8 columns, 4 words,

@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(128) grouped_gemv_kernel(
         float v0 = acc[0][j][h] * gs, v1 = acc[0][j][h + 2] * gs;
         if (SWI) {
           const float gu = (FMT == 3) ? up.g : 1.0f;
-          v0 = v0 / (1.0f + expf(-v0)) * (acc[kMats - 1][j][h] * gu);
-          v1 = v1 / (1.0f + expf(-v1)) * (acc[kMats - 1][j][h + 2] * gu);
+          v0 = silu_fast(v0) * (acc[kMats - 1][j][h] * gu);
+          v1 = silu_fast(v1) * (acc[kMats - 1][j][h + 2] * gu);
         }
         const int64_t pr = perm ? perm[start + tok0 + slot] : start + tok0 + slot;
         if (r0 < n) y[pr * n + r0] = f32_to_f16_bits(v0);
