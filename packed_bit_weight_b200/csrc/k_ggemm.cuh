@@ -12,7 +12,9 @@
 // 1,100 cycles of the 128-byte port for 512 cycles of MMA; with the weights
 // in TMEM the port carries X once in and once out and the lookups, ~650.
 // On B200, 32 IQ4_NL experts over 8,192 rows: gate and up (896 x 2560 each)
-// 114 us, 660 TFLOP/s; down (2560 x 896) 66 us.  What bounds it: the decode's
+// 116 to 122 us, 620 to 650 TFLOP/s, from box to box; down (2560 x 896) 66 to
+// 69 us; gate and up in FP4-G16, E4M3 and MXFP4 110, 107 and 110 us where IQ4_NL
+// takes 119.  What bounds it: the decode's
 // latency (434 ns per step at 16 rows, 262 with the lookups left out, 208 with
 // copies and X left out too; the MMAs of 256 rows are 260), and 5 rounds of
 // tiles where 4.5 would do.

@@ -1037,7 +1037,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         tc_fence_before();
         warp_arrive(acce + 8 * a, lane);
       } else if (u + 1 == my_units || ch + 1 == nch) {
-        // the tile's last unit is the other group's: wait for its products too,
+        // the tile's last unit is another group's: wait for its products too,
         // so that h may be written again
         ok = gg_wait(accf + 8 * (c & 3u), (c >> 2) & 1u);
         ok = __all_sync(0xFFFFFFFFu, ok);

@@ -1609,10 +1609,17 @@ static qmm_status check_adapters(const qmm_adapters* ad) {
 
 // A cluster per row (lora_token_kernel: no sort, one launch, A and B read once
 // per row) while that reads little, else the tiled path, which reads them once
-// per tile but has three launches.  On B200, us, cluster per row / tiled (rows
-// of four adapters): 32 rows, rank 16, 4096 -> 18560 (23 MB): 16.4 / 21.5; 16
-// rows of rank 64 (46 MB): 22.6 / 23.6; 24 (70 MB): 30.7 / 23.5; 64 rows of
-// rank 16: 24.6 / 23.6.
+// per tile but has three launches.  On B200, us a call, cluster per row / tiled,
+// 4096 -> 18560, with rows of four adapters and with an adapter each:
+//   16 rows, rank 16 (5.8 M)    8.0 / 18.4     8.0 / 22.5
+//   64 rows, rank 16 (23 M)    16.3 / 22.5    21.7 / 48.4
+//   16 rows, rank 64 (23 M)    16.0 / 18.4    18.7 / 28.7
+//   32 rows, rank 64 (46 M)    24.4 / 18.4    28.9 / 37.0
+//   64 rows, rank 64 (93 M)    46.2 / 24.2    55.1 / 55.3
+// and 8192 -> 4096: 32 rows, rank 64 (25 M) 12.5 / 20.5 and 20.2 / 30.6; 64 rows
+// (50 M) 24.1 / 28.6 and 35.3 / 41.5.  The ids are on the device, so the rule
+// cannot tell few adapters from many: it takes the range in which a cluster per
+// row wins with both.
 static bool lora_by_row(const qmm_adapters* ad, int64_t m) {
   return m <= 64 && m * ad->rank * (ad->n + ad->k) <= (int64_t)24 << 20;
 }
