@@ -153,8 +153,8 @@ class PackedWeights:
 
     def desc(self) -> qmm_weights:
         """The C descriptor, rebuilt only when a field or a buffer changed."""
-        key = (self.fmt, self.n, self.k, None if self.data is None else (self.data.data_ptr(), self.data.numel()),
-               None if self.scales is None else (self.scales.data_ptr(), self.scales.numel()), self.global_scale,
+        key = (self.fmt, self.n, self.k, None if self.data is None else (self.data.data_ptr(), self.data.nbytes),
+               None if self.scales is None else (self.scales.data_ptr(), self.scales.nbytes), self.global_scale,
                self.experts, self.data_stride, self.scale_stride)
         cached = self.__dict__.get("_desc")
         if cached is not None and cached[0] == key:

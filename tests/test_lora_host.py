@@ -52,3 +52,19 @@ def test_bfloat16_is_refused_where_values_are_calculated_with():
             qmm.Adapters(z(4, 16, 256, dt=dt), z(4, 64, 16), z(4, dt=torch.float32)).desc()
     with pytest.raises(ValueError, match="CUDA"):
         qmm.qmm_permute(bf(8, 64), rows, bf(16, 64))       # copied: any 2-byte type
+
+
+def test_packed_weights_of_another_size_at_the_same_address_are_checked_again():
+    """As many scales, at the same address, in half the bytes."""
+    n, k, E = 64, 256, 2
+    fmt = qmm.FMT_FP4G16_F16
+    data = torch.zeros(E * qmm.qmm_data_bytes(fmt, n, k), dtype=torch.uint8)
+    scales = torch.zeros(E * n * k // 16, dtype=torch.float16)
+    w = qmm.PackedWeights(fmt, n, k, data, scales, 1.0, E)
+    assert w.desc().expert_scale_stride == scales.nbytes // E
+    w.scales = scales.view(torch.uint8)[:scales.numel()]
+    assert w.scales.data_ptr() == scales.data_ptr() and w.scales.numel() == scales.numel()
+    with pytest.raises(ValueError, match="scales holds"):
+        w.desc()
+    w.scales = scales
+    assert w.desc().expert_scale_stride == scales.nbytes // E
